@@ -66,7 +66,7 @@ enum {
     TW_ERR_NULL = 1,       /* a required pointer is NULL                    */
     TW_ERR_SHAPE = 2,      /* N < 1, M < 1, K < 1, K % 128 != 0, or too big */
     TW_ERR_ALIGN = 3,      /* a pointer is not 16-byte aligned              */
-    TW_ERR_BUFSIZE = 4,    /* a buffer or workspace is smaller than needed  */
+    TW_ERR_BUFSIZE = 4,    /* a buffer, workspace or free list is too small */
     TW_ERR_NONFINITE = 5,  /* W holds Inf or NaN (reported by tw_check)     */
     TW_ERR_CUDA = 6,       /* a CUDA runtime call failed                    */
     TW_ERR_TIMEOUT = 7,    /* a bounded device-side wait expired (tw_check) */
@@ -487,6 +487,192 @@ TW_API int tw_quantize_act_given(const float *x, int64_t M, int64_t K, const flo
  */
 TW_API int tw_rescale_acc(const int32_t *acc, int64_t M, int64_t N, const float *amax,
                           const float *wscale, float *y, tw_stream_t stream);
+
+/*
+ * Paged key-value cache
+ * ---------------------
+ * What a decoder layer does between its projections: the "KV cache" that
+ * decoder_model_merged maps beside its inputs_embeds ("VibeVoice-ASR-BitNet-
+ * ONNX" model page, "Layout").  The pages name the cache and give no layout;
+ * this one is the library's own.  Keys and values of one layer lie in two
+ * pools of pages, page_size tokens to a page; a request's i-th page is entry
+ * i of its row of the block table, and a token's slot is
+ * page * page_size + its place in the page.
+ *
+ * int32 and fp32 arrays of this section need the alignment of their type;
+ * pools and fp32 rows are 16-byte aligned (strides included).
+ */
+#define TW_KV_BF16 0
+#define TW_KV_F16 1
+#define TW_KV_I8 2   /* codes with one fp32 scale per token and head:        */
+                     /* value = code * scale, scale = absmax / 127           */
+typedef struct tw_kv_cache {
+    void *k, *v;                /* element (page, token, head, c) of either  */
+                                /* pool at page * page_stride + token *      */
+                                /* token_stride + head * head_stride + c     */
+    float *k_scale, *v_scale;   /* TW_KV_I8: [num_pages x page_size x        */
+                                /* kv_heads], contiguous; else NULL          */
+    int64_t num_pages, page_size, kv_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;   /* in elements         */
+    int64_t dtype;              /* TW_KV_*                                   */
+} tw_kv_cache;
+/* head_dim: a multiple of 8 (TW_KV_I8: of 16), at most 256; num_pages *
+ * page_size < 2^31; strides a multiple of 16 bytes and >= head_dim. */
+
+/*
+ * Block tables, slots and positions of one step, from lengths on the GPU.
+ * Request r goes from lengths[r] tokens to max(0, lengths[r] + delta[r]).
+ *  - A request that shrinks hands back the pages it no longer needs (entries
+ *    ceil(new / page_size) .. ceil(old / page_size) - 1 of its table row):
+ *    they are written on top of the free list, request by request, each
+ *    request's in table order.  The table entries stay as they were.
+ *  - A request that grows then takes the pages it needs from the top of the
+ *    list, request by request in the same order, into its table row.
+ *  - Every new token of a growing request gets one row, request by request:
+ *    slots[t], positions[t] (its place in the request, from 0) and
+ *    request_of_row[t].  Rows behind the last new token get -1, 0 and -1.
+ *    row_start[r] is the first row of request r, row_start[requests] the
+ *    number of rows used (row_start may be NULL).
+ * The free list is free_pages[0 .. free_count - 1] of free_capacity entries.
+ * lengths_out may be lengths and free_count_out free_count; delta is read
+ * only.  A step is taken whole or not at all: if there are too few free
+ * pages, table columns (max_pages) or rows, TW_ERR_BUFSIZE is recorded, if a
+ * length is negative or a count does not fit its array, TW_ERR_CORRUPT (both
+ * returned by tw_check); then the table and the list are left as they were,
+ * the lengths and the count are copied, every row gets -1, 0 and -1 and
+ * row_start zeros.
+ * 1 <= requests <= 8192, 0 <= rows < 2^31.  One launch.
+ */
+#define TW_KV_MAX_REQUESTS 8192
+TW_API int tw_kv_assign(const int32_t *lengths, const int32_t *delta, int64_t requests,
+                        int64_t page_size, int32_t *block_table, int64_t max_pages,
+                        int64_t table_stride, int32_t *free_pages, int64_t free_capacity,
+                        const int32_t *free_count, int32_t *lengths_out, int32_t *free_count_out,
+                        int32_t *slots, int32_t *positions, int32_t *request_of_row, int64_t rows,
+                        int32_t *row_start, tw_stream_t stream);
+
+/*
+ * Rotate the new tokens' queries and keys by their positions and write keys
+ * and values into their slots.  Per row t: q [heads x head_dim], k and v
+ * [kv_heads x head_dim] fp32 with row strides ldq, ldk, ldv; the first
+ * `rotary` columns of each head of q and k are rotated in pairs by the
+ * angles positions[t] * inv_freq[i], i < rotary / 2 (fp64, formed and reduced
+ * in fp64), the pair i being columns (i, i + rotary/2), or (2i, 2i + 1) when
+ * interleaved:  (a, b) -> (a cos - b sin, b cos + a sin) in fp32.  q_out
+ * (row stride ldqo; may be q with the same stride) receives every row's
+ * queries.  Keys and values of a row with slots[t] < 0 are not written; a
+ * slot at or past the end of the pools records TW_ERR_CORRUPT and is not
+ * written either.  Slots of different rows must differ.  TW_KV_I8: amax =
+ * max |x| over the head, code = clamp(rint(x * (127.0f / amax)), -127, 127),
+ * scale = amax / 127.0f (amax == 0: code 0); non-finite values give
+ * unspecified codes.
+ * rotary: a multiple of 8, 0 <= rotary <= head_dim (0: inv_freq unused).
+ */
+TW_API int tw_rope_append(const float *q, int64_t ldq, const float *k, int64_t ldk, const float *v,
+                          int64_t ldv, int64_t rows, int64_t heads, int64_t rotary,
+                          const double *inv_freq, int interleaved, const int32_t *positions,
+                          const int32_t *slots, const tw_kv_cache *cache, float *q_out,
+                          int64_t ldqo, tw_stream_t stream);
+
+/* HOST-ONLY.  Scratch of tw_paged_attention (0 for arguments that it
+ * refuses).  It must be zero-filled before its first use; every call leaves
+ * its counters zero again.  One workspace serves one call at a time: calls
+ * that may run at once on the GPU, captured graphs among them, need one each. */
+TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads, int64_t kv_heads,
+                                                 int64_t head_dim);
+
+/*
+ * Attention of one new token per request over its cached keys and values.
+ * Query head i of request r (q [requests x heads * head_dim], row stride
+ * ldq) sees keys j of KV head i / (heads / kv_heads) with
+ * max(0, first[r]) <= j < lengths[r] (first NULL: from 0):
+ *   s_j = scale * (q_i . k_j);  m = max s_j
+ *   out_i = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m);  lse_i = m + log sum_j e^(s_j - m)
+ * A request that sees no key gets out = 0 and lse = -inf.  out has row stride
+ * ldo; lse [requests x heads] may be NULL.  Nothing outside the visible keys
+ * is used, whatever its pages hold.  A length past max_pages * page_size and
+ * a page outside the pools record TW_ERR_CORRUPT: the keys concerned are left
+ * out.  Sums and softmax statistics are fp32; the products' operands are
+ * carried with at least 21 significant bits (cache elements exactly).
+ * TW_KV_I8: the scales of visible keys and values are 0 or in
+ * [2^-60, 2^60].  heads: a multiple of kv_heads.
+ */
+TW_API int tw_paged_attention(const float *q, int64_t ldq, int64_t requests, int64_t heads,
+                              const tw_kv_cache *cache, const int32_t *block_table,
+                              int64_t max_pages, int64_t table_stride, const int32_t *lengths,
+                              const int32_t *first, float scale, float *out, int64_t ldo,
+                              float *lse, void *ws, size_t ws_bytes, tw_stream_t stream);
+
+/*
+ * Residual sum between two blocks with their norms
+ * ------------------------------------------------
+ * Per row of K columns (fp32, row strides ld*):
+ *   t = post(y);  h = x + alpha * gate * t;  n = pre(h)
+ * with post and pre one of
+ *   TW_NORM_NONE   u
+ *   TW_NORM_RMS    u / sqrt(mean(u^2) + eps) * w
+ *   TW_NORM_LAYER  (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps) * w + b
+ * Weights and biases [K] may be NULL (1 and 0; a bias goes with
+ * TW_NORM_LAYER only).  gate: NULL (1), one row for all rows (ldgate 0), or
+ * a row each.  y NULL: h = x (post, gate and alpha are not used).
+ * Outputs, each optional but one at least: h (may be x with the same
+ * stride), n (may be y or x likewise; a different buffer than h), and the
+ * int8 codes of n for the next projection as tw_quantize_act makes them
+ * (xq [M x K], amax [M], and qsum [M] or NULL), bit for bit.
+ * 1 <= K <= 32768; sums in fp32.  One launch.
+ */
+#define TW_NORM_NONE 0
+#define TW_NORM_RMS 1
+#define TW_NORM_LAYER 2
+typedef struct tw_residual_norm_args {
+    const float *x, *y, *gate;
+    const float *post_weight, *post_bias, *pre_weight, *pre_bias;
+    float *h, *n;
+    int8_t *xq;
+    float *amax;
+    int32_t *qsum;
+    int64_t M, K, ldx, ldy, ldgate, ldh, ldn;
+    int32_t post, pre;
+    float alpha, eps;
+} tw_residual_norm_args;
+TW_API int tw_residual_norm(const tw_residual_norm_args *args, tw_stream_t stream);
+
+/*
+ * The decoder-layer chain with its cache and norms
+ * ------------------------------------------------
+ * The layers of tw_decoder_chain, one new token per request, with what that
+ * leaves out.  Per layer, x [M x hidden] being the residual stream:
+ *   h = rms(x) * norm_in;  q, k, v = projections of h
+ *   rotate q and k, append k and v to the layer's cache, a = attention
+ *   x = x + o(a);  h1 = rms(x) * norm_mid
+ *   x = x + down(SiLU(gate(h1)) * up(h1))
+ * and behind the last layer h = rms(x) * norm_out.  The tables are those of
+ * tw_chain_layer, with q's y = q and k's y = k.  M requests; positions, slots
+ * and lengths as tw_kv_assign writes them for one new token each.  Every
+ * table is checked before anything is launched.
+ */
+typedef struct tw_cached_layer {
+    tw_kv_cache cache;                    /* kv_heads * head_dim = kv_dim     */
+    const float *norm_in, *norm_mid;      /* [hidden] gains                   */
+} tw_cached_layer;
+typedef struct tw_chain_cache {
+    float *x;                             /* [M x hidden], in and out         */
+    float *q, *k;                         /* [M x hidden], [M x kv_dim]       */
+    const float *norm_out;                /* [hidden]                         */
+    const int32_t *positions, *slots;     /* [M]                              */
+    const int32_t *block_table;
+    const int32_t *lengths, *first;       /* [M]; first may be NULL           */
+    const double *inv_freq;               /* [rotary / 2]                     */
+    int64_t max_pages, table_stride, rotary;
+    int32_t interleaved;
+    float scale, eps;
+    void *attention_ws;                   /* tw_paged_attention's workspace   */
+    size_t attention_ws_bytes;
+} tw_chain_cache;
+TW_API int tw_decoder_chain_cached(const tw_chain_layer *layers, const tw_cached_layer *cached,
+                                   int n_layers, const tw_chain_buffers *buf,
+                                   const tw_chain_cache *c, void *ws, size_t ws_bytes,
+                                   tw_stream_t stream);
 
 /* Wait for `stream`, then return and clear the device error word of the
  * current device (TW_OK if no kernel reported an error). */

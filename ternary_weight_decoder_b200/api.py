@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Sequence
+from typing import NamedTuple, Sequence
 
 import torch
 
@@ -452,3 +452,439 @@ def rescale_acc(acc: torch.Tensor, amax: torch.Tensor, wscale: torch.Tensor, y=N
         y = torch.empty((M, N), dtype=torch.float32, device=acc.device)
     _raise(tw_rescale_acc(_ptr(acc), M, N, _ptr(amax), _ptr(wscale), _ptr(y), _stream(stream)))
     return y
+
+
+# ------------------------------------------------ paged key-value cache
+KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.int8: 2}   # TW_KV_*
+KV_MAX_REQUESTS = 8192
+
+
+class KVCacheStruct(ctypes.Structure):
+    """Mirror of ``tw_kv_cache``."""
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("num_pages", _i64),
+                ("page_size", _i64), ("kv_heads", _i64), ("head_dim", _i64), ("page_stride", _i64),
+                ("token_stride", _i64), ("head_stride", _i64), ("dtype", _i64)]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of ``tw_residual_norm_args``."""
+    _fields_ = [(n, _p) for n in ("x", "y", "gate", "post_weight", "post_bias", "pre_weight",
+                                  "pre_bias", "h", "n", "xq", "amax", "qsum")] + \
+        [(n, _i64) for n in ("M", "K", "ldx", "ldy", "ldgate", "ldh", "ldn")] + \
+        [("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("alpha", ctypes.c_float),
+         ("eps", ctypes.c_float)]
+
+
+class CachedLayer(ctypes.Structure):
+    """Mirror of ``tw_cached_layer``."""
+    _fields_ = [("cache", KVCacheStruct), ("norm_in", _p), ("norm_mid", _p)]
+
+
+class ChainCache(ctypes.Structure):
+    """Mirror of ``tw_chain_cache``."""
+    _fields_ = [("x", _p), ("q", _p), ("k", _p), ("norm_out", _p), ("positions", _p), ("slots", _p),
+                ("block_table", _p), ("lengths", _p), ("first", _p), ("inv_freq", _p),
+                ("max_pages", _i64), ("table_stride", _i64), ("rotary", _i64),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("attention_ws", _p), ("attention_ws_bytes", _sz)]
+
+
+_f32 = ctypes.c_float
+tw_kv_assign = _sig("tw_kv_assign", _int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _p,
+                                           _p, _p, _p, _i64, _p, _p])
+tw_rope_append = _sig("tw_rope_append", _int, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p,
+                                               _int, _p, _p, _p, _p, _i64, _p])
+tw_paged_attention_workspace_bytes = _sig("tw_paged_attention_workspace_bytes", _sz,
+                                          [_i64, _i64, _i64, _i64])
+tw_paged_attention = _sig("tw_paged_attention", _int, [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p,
+                                                       _p, _f32, _p, _i64, _p, _p, _sz, _p])
+tw_residual_norm = _sig("tw_residual_norm", _int, [_p, _p])
+tw_decoder_chain_cached = _sig("tw_decoder_chain_cached", _int,
+                               [_p, _p, _int, _p, _p, _p, _sz, _p])
+
+
+def _launch(call, device, stream, used):
+    """Run ``call(raw_stream)`` on ``device`` and raise on its status.  With a
+    stream other than the current one, the tensors in ``used`` are kept from
+    reuse until that stream has passed this point."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(call, device, stream, used)
+    current = torch._C._cuda_getCurrentRawStream(index)
+    raw = current if stream is None else stream.cuda_stream
+    status = call(raw)
+    if status:
+        _raise(status)
+    if raw != current:
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _new(size, dtype, device, stream):
+    """An output made on the stream that writes it."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
+def _want(t, dtype, shape, name, device):
+    """A contiguous tensor of this type, shape (None: any size) and device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a tensor of {dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+
+
+def _want_rows(t, shape, name, device):
+    """An fp32 matrix whose rows are contiguous (any row stride); returns the stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a tensor of torch.float32")
+    if len(t.shape) != 2 or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    ld, last = t.stride()
+    if last != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] <= 1:
+        return -(-t.shape[1] // 4) * 4   # one row has no stride of its own
+    return ld
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+class KVCache:
+    """Key and value pools [num_pages, page_size, kv_heads, head_dim] of one
+    layer (bfloat16, float16, or int8 codes with fp32 scales [num_pages,
+    page_size, kv_heads], value = code * scale).  Any strides, the same for
+    both pools, with the last dimension contiguous.  The handle holds the
+    tensors."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        self.device = _cuda_device(k, "k")
+        if k.dtype not in KV_DTYPES:
+            raise TypeError(f"pools must be one of {list(KV_DTYPES)}, got {k.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+            raise ValueError("k and v must be alike: [num_pages, page_size, kv_heads, head_dim]")
+        # A dimension of size 1 has no stride of its own.
+        strides = [s if n > 1 else 0 for n, s in zip(k.shape, k.stride())]
+        if strides != [s if n > 1 else 0 for n, s in zip(v.shape, v.stride())]:
+            raise ValueError("k and v must have the same strides")
+        if k.shape[3] > 1 and k.stride(3) != 1:
+            raise ValueError("the head dimension of the pools must be contiguous")
+        if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("int8 pools come with k_scale and v_scale, others without")
+        if k_scale is not None:
+            _want(k_scale, torch.float32, k.shape[:3], "k_scale", self.device)
+            _want(v_scale, torch.float32, k.shape[:3], "v_scale", self.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        strides = [s or -(-self.head_dim // 16) * 16 for s in strides]
+        self.struct = KVCacheStruct(_data(k), _data(v), _data(k_scale), _data(v_scale), *k.shape,
+                                    *strides[:3], KV_DTYPES[k.dtype])
+        self.ref = ctypes.addressof(self.struct)
+        self.tensors = (k, v, k_scale, v_scale)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
+              dtype=torch.bfloat16, device="cuda"):
+        """A cache of new pools (zeros)."""
+        size = (num_pages, page_size, kv_heads, head_dim)
+        pools = [torch.zeros(size, dtype=dtype, device=device) for _ in range(2)]
+        scales = [torch.zeros(size[:3], device=device) for _ in range(2)] if dtype == torch.int8 else []
+        return cls(*pools, *scales)
+
+
+class KVAssignment(NamedTuple):
+    """What ``kv_assign`` gives, all int32: the lengths after the step
+    [requests], the free pages left [1], one slot, position and request per
+    row [rows], and the first row of each request [requests + 1]."""
+    lengths: torch.Tensor
+    free_count: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    requests: torch.Tensor
+    row_start: torch.Tensor
+
+
+def kv_assign(lengths: torch.Tensor, delta: torch.Tensor, block_table: torch.Tensor,
+              free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, rows: int,
+              lengths_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+              stream=None) -> KVAssignment:
+    """One step of a paged cache from lengths on the GPU: request r goes from
+    lengths[r] to max(0, lengths[r] + delta[r]) tokens; pages go back to and
+    come from the free list, ``block_table`` [requests, max_pages] (any row
+    stride) and ``free_pages`` are updated in place, and each new token gets a
+    row.  ``lengths_out`` and ``free_count_out`` may be the inputs themselves.
+    A step that does not fit changes nothing and is reported by ``check``."""
+    device = _cuda_device(lengths, "lengths")
+    i32 = torch.int32
+    _want(lengths, i32, (None,), "lengths", device)
+    n = lengths.shape[0]
+    _want(delta, i32, (n,), "delta", device)
+    _want(free_pages, i32, (None,), "free_pages", device)
+    _want(free_count, i32, (1,), "free_count", device)
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != i32:
+        raise TypeError(f"block_table must be a tensor of {i32}")
+    if block_table.dim() != 2 or block_table.shape[0] != n or block_table.device != device or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [requests, max_pages] with contiguous rows, beside lengths")
+    width = block_table.shape[1]
+    stride = block_table.stride(0) if n > 1 else width
+    if rows < 0:
+        raise ValueError("rows must be >= 0")
+    if lengths_out is None:
+        lengths_out = _new(n, i32, device, stream)
+    else:
+        _want(lengths_out, i32, (n,), "lengths_out", device)
+    if free_count_out is None:
+        free_count_out = _new(1, i32, device, stream)
+    else:
+        _want(free_count_out, i32, (1,), "free_count_out", device)
+    per_row = _new((3, rows), i32, device, stream)
+    slots, positions, requests = per_row.unbind(0)
+    row_start = _new(n + 1, i32, device, stream)
+    at = per_row.data_ptr()
+    _launch(lambda s: tw_kv_assign(
+        lengths.data_ptr(), delta.data_ptr(), n, page_size, block_table.data_ptr(), width, stride,
+        free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), lengths_out.data_ptr(),
+        free_count_out.data_ptr(), at, at + 4 * rows, at + 8 * rows, rows, row_start.data_ptr(), s),
+        device, stream, (lengths, delta, block_table, free_pages, free_count, lengths_out,
+                         free_count_out, per_row, row_start))
+    return KVAssignment(lengths_out, free_count_out, slots, positions, requests, row_start)
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                slots: torch.Tensor, cache: KVCache, inv_freq: torch.Tensor | None = None,
+                interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None):
+    """Rotate q [rows, heads * head_dim] and k [rows, kv_heads * head_dim] by
+    positions [rows] * inv_freq [rotary / 2] (fp64; None: no rotation), write
+    k and v into the cache at slots [rows] (negative: not written) and return
+    the rotated queries (``q_out``; may be q).  Rows may be strided."""
+    device = _cuda_device(q, "q")
+    wide = cache.kv_heads * cache.head_dim
+    ldq = _want_rows(q, (None, None), "q", device)
+    rows, width = q.shape
+    if width % cache.head_dim:
+        raise ValueError(f"q has {width} columns, not whole heads of {cache.head_dim}")
+    ldk = _want_rows(k, (rows, wide), "k", device)
+    ldv = _want_rows(v, (rows, wide), "v", device)
+    _want(positions, torch.int32, (rows,), "positions", device)
+    _want(slots, torch.int32, (rows,), "slots", device)
+    if cache.device != device:
+        raise ValueError(f"the cache must be on {device}, is on {cache.device}")
+    rotary = 0
+    if inv_freq is not None:
+        _want(inv_freq, torch.float64, (None,), "inv_freq", device)
+        rotary = 2 * inv_freq.shape[0]
+    if q_out is None:
+        q_out = _new((rows, width), torch.float32, device, stream)
+    ldqo = _want_rows(q_out, (rows, width), "q_out", device)
+    _launch(lambda s: tw_rope_append(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, width // cache.head_dim, rotary,
+        inv_freq.data_ptr() if rotary else None, interleaved, positions.data_ptr(), slots.data_ptr(),
+        cache.ref, q_out.data_ptr(), ldqo, s),
+        device, stream, (q, k, v, positions, slots, inv_freq, q_out) + cache.tensors)
+    return q_out
+
+
+def paged_attention_workspace(requests: int, heads: int, cache: KVCache) -> torch.Tensor:
+    """Zeroed scratch for ``paged_attention`` calls of up to this many requests
+    and heads on the cache, one call at a time."""
+    n = int(tw_paged_attention_workspace_bytes(requests, heads, cache.kv_heads, cache.head_dim))
+    if not n:
+        raise ValueError(f"no attention of {requests} requests, {heads} heads over {cache.kv_heads}")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lengths: torch.Tensor,
+                    first: torch.Tensor | None = None, scale: float | None = None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None, return_lse: bool = False, stream=None):
+    """Attention of one new token per request, q [requests, heads * head_dim],
+    over keys max(0, first[r]) .. lengths[r] - 1 of its pages in block_table
+    [requests, max_pages]; scale is 1 / sqrt(head_dim) by default.  Returns out,
+    or (out, lse) with the log-sum-exps [requests, heads].  ``ws`` comes from
+    ``paged_attention_workspace`` (None: one is made for the call)."""
+    device = _cuda_device(q, "q")
+    ldq = _want_rows(q, (None, None), "q", device)
+    n, width = q.shape
+    if width % cache.head_dim:
+        raise ValueError(f"q has {width} columns, not whole heads of {cache.head_dim}")
+    heads = width // cache.head_dim
+    if cache.device != device:
+        raise ValueError(f"the cache must be on {device}, is on {cache.device}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
+        raise TypeError("block_table must be a tensor of torch.int32")
+    if block_table.dim() != 2 or block_table.shape[0] != n or block_table.device != device or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [requests, max_pages] with contiguous rows, beside q")
+    pages = block_table.shape[1]
+    stride = block_table.stride(0) if n > 1 else pages
+    _want(lengths, torch.int32, (n,), "lengths", device)
+    if first is not None:
+        _want(first, torch.int32, (n,), "first", device)
+    if out is None:
+        out = _new((n, width), torch.float32, device, stream)
+    ldo = _want_rows(out, (n, width), "out", device)
+    if lse is not None:
+        _want(lse, torch.float32, (n, heads), "lse", device)
+    elif return_lse:
+        lse = _new((n, heads), torch.float32, device, stream)
+    if ws is None:
+        if stream is None:
+            ws = paged_attention_workspace(n, heads, cache)
+        else:
+            with torch.cuda.stream(stream):
+                ws = paged_attention_workspace(n, heads, cache)
+    else:
+        _want(ws, torch.uint8, (None,), "ws", device)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    _launch(lambda s: tw_paged_attention(
+        q.data_ptr(), ldq, n, heads, cache.ref, block_table.data_ptr(), pages, stride,
+        lengths.data_ptr(), _data(first), scale, out.data_ptr(), ldo, _data(lse), ws.data_ptr(),
+        ws.shape[0], s),
+        device, stream, (q, block_table, lengths, first, out, lse, ws) + cache.tensors)
+    return (out, lse) if return_lse else out
+
+
+# -------------------------------------------- residual sum with its norms
+NORMS = {None: 0, "rms": 1, "layer": 2}   # TW_NORM_*
+
+
+class NormResult(NamedTuple):
+    """h [M, K]; n [M, K] or, quantised, xq int8 [M, K], amax [M], qsum [M]."""
+    h: torch.Tensor
+    n: torch.Tensor | None = None
+    xq: torch.Tensor | None = None
+    amax: torch.Tensor | None = None
+    qsum: torch.Tensor | None = None
+
+
+def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str | None = None,
+                  post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, alpha: float = 1.0, pre: str | None = "rms",
+                  pre_weight: torch.Tensor | None = None, pre_bias: torch.Tensor | None = None,
+                  eps: float = 1e-6, h: torch.Tensor | None = None, n: torch.Tensor | None = None,
+                  quantize: bool = False, stream=None) -> NormResult:
+    """h = x + alpha * gate * post(y) and n = pre(h) per row of x, y [M, K]
+    (rows may be strided); post and pre are None, "rms" or "layer" with their
+    weights and biases [K]; gate is [K], [M, K] or None.  Without y, h is x.
+    ``quantize`` gives the int8 codes of n (as ``quantize_act``) in its
+    place, ready for ``ternary_linear_q``.  h and n may be passed in, h may be
+    x and n may be y."""
+    device = _cuda_device(x, "x")
+    ldx = _want_rows(x, (None, None), "x", device)
+    size = x.shape
+    rows, width = size
+    if post not in NORMS or pre not in NORMS:
+        raise ValueError(f"post and pre must be one of {list(NORMS)}")
+    ldy = 0 if y is None else _want_rows(y, size, "y", device)
+    ldg = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            _want(gate, torch.float32, (width,), "gate", device)
+        else:
+            ldg = _want_rows(gate, size, "gate", device)
+    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
+                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        if t is not None:
+            _want(t, torch.float32, (width,), name, device)
+    if quantize and n is not None:
+        raise ValueError("quantize gives codes: n cannot be passed in")
+    ldh = ldn = 0
+    if y is None and h is None:
+        out_h = None   # h is x as it stands
+    else:
+        out_h = _new(size, torch.float32, device, stream) if h is None else h
+        ldh = _want_rows(out_h, size, "h", device)
+    xq = amax = qsum = None
+    if quantize:
+        xq = _new(size, torch.int8, device, stream)
+        amax = _new(rows, torch.float32, device, stream)
+        qsum = _new(rows, torch.int32, device, stream)
+    elif pre is not None or n is not None:
+        n = _new(size, torch.float32, device, stream) if n is None else n
+        ldn = _want_rows(n, size, "n", device)
+    elif out_h is None:
+        raise ValueError("nothing to compute: no y, no norm and no codes")
+    args = NormArgs(x.data_ptr(), _data(y), _data(gate), _data(post_weight), _data(post_bias),
+                    _data(pre_weight), _data(pre_bias), _data(out_h), _data(n), _data(xq),
+                    _data(amax), _data(qsum), rows, width, ldx, ldy, ldg, ldh, ldn, NORMS[post],
+                    NORMS[pre], alpha, eps)
+    _launch(lambda s: tw_residual_norm(ctypes.byref(args), s), device, stream,
+            (x, y, gate, post_weight, post_bias, pre_weight, pre_bias, out_h, n, xq, amax, qsum))
+    return NormResult(x if out_h is None else out_h, n, xq, amax, qsum)
+
+
+# ------------------------------------- decoder-layer chain with its cache
+class CachedDecoderChain(DecoderChain):
+    """A ``DecoderChain`` whose layers attend over a paged cache and have
+    their norms: ``x`` [M, hidden] is the residual stream, in and out, and
+    ``h`` the last norm's output.  ``caches`` is one ``KVCache`` per layer,
+    ``norms`` one (norm_in, norm_mid) pair of gains per layer, ``norm_out``
+    the last gain.  ``block_table`` [M, max_pages], ``lengths`` [M] (counting
+    the new token), ``positions`` [M] and ``slots`` [M] are int32 tensors that
+    every run reads, as ``kv_assign`` fills them for one new token each."""
+
+    def __init__(self, layers, M: int, hidden: int, kv_dim: int, head_dim: int, inter: int, device,
+                 caches, norms, norm_out, inv_freq, block_table, lengths, positions, slots,
+                 first=None, scale: float | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, acc_out=None):
+        super().__init__(layers, M, hidden, kv_dim, head_dim, inter, device, acc_out=acc_out)
+        if len(caches) != len(layers) or len(norms) != len(layers):
+            raise ValueError("one cache and one pair of norm gains per layer")
+        dev = self.h.device
+        for t, name in ((lengths, "lengths"), (positions, "positions"), (slots, "slots"), (first, "first")):
+            if t is not None or name != "first":
+                _want(t, torch.int32, (M,), name, dev)
+        _want(block_table, torch.int32, (M, None), "block_table", dev)
+        if inv_freq is not None:
+            _want(inv_freq, torch.float64, (None,), "inv_freq", dev)
+        _want(norm_out, torch.float32, (hidden,), "norm_out", dev)
+        for pair in norms:
+            for t in pair:
+                _want(t, torch.float32, (hidden,), "norm gain", dev)
+        for c in caches:
+            if c.device != dev:
+                raise ValueError(f"the caches must be on {dev}")
+        self.x = torch.zeros((M, hidden), dtype=torch.float32, device=dev)
+        self.caches, self.norms, self.norm_out = list(caches), list(norms), norm_out
+        self.inv_freq, self.block_table, self.lengths = inv_freq, block_table, lengths
+        self.positions, self.slots, self.first = positions, slots, first
+        self.attention_ws = paged_attention_workspace(M, hidden // head_dim, self.caches[0])
+        self.c_cached = (CachedLayer * len(layers))()
+        for i, (c, (a, b)) in enumerate(zip(self.caches, self.norms)):
+            self.c_cached[i] = CachedLayer(c.struct, _data(a), _data(b))
+        self.c_cache = ChainCache(
+            _data(self.x), _data(self.q), _data(self.k), _data(norm_out), _data(positions),
+            _data(slots), _data(block_table), _data(lengths), _data(first), _data(inv_freq),
+            block_table.shape[1], block_table.shape[1],
+            0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved),
+            head_dim ** -0.5 if scale is None else scale, eps, _data(self.attention_ws),
+            self.attention_ws.numel())
+
+
+def decoder_chain_cached(chain: CachedDecoderChain, stream=None):
+    """Run every layer of ``chain`` for one new token per request."""
+    _launch(lambda s: tw_decoder_chain_cached(
+        chain.c_layers, chain.c_cached, chain.n_layers, ctypes.byref(chain.c_buf),
+        ctypes.byref(chain.c_cache), chain.ws.data_ptr(), chain.ws_bytes, s),
+        chain.h.device, stream, ())

@@ -763,6 +763,9 @@ int tw_check(tw_stream_t stream)
         return fail(TW_ERR_TIMEOUT, "a device-side wait timed out (error word 0x%x)", v);
     if (v & tw::EFLAG_NONFINITE)
         return fail(TW_ERR_NONFINITE, "non-finite weight found (error word 0x%x)", v);
+    if ((v & tw::EFLAG_NOSPACE) && !(v & tw::EFLAG_BADDESC))
+        return fail(TW_ERR_BUFSIZE, "too few free pages, block-table columns or rows for a step "
+                    "(error word 0x%x)", v);
     return fail(TW_ERR_CORRUPT, "kernel reported a malformed descriptor (error word 0x%x)", v);
 }
 
@@ -1013,6 +1016,98 @@ int tw_decoder_chain(const tw_chain_layer *layers, int n_layers, const tw_chain_
             return cuda_fail(e, "chain residual launch");
     }
     return TW_OK;
+}
+
+int tw_decoder_chain_cached(const tw_chain_layer *layers, const tw_cached_layer *cached,
+                            int n_layers, const tw_chain_buffers *buf, const tw_chain_cache *c,
+                            void *ws, size_t ws_bytes, tw_stream_t stream)
+{
+    t_last_error[0] = 0;
+    const char *who = "tw_decoder_chain_cached";
+    if (!layers || !cached || n_layers < 1)
+        return fail(TW_ERR_NULL, "%s: at least one layer required", who);
+    if (int rc = check_chain_buffers(buf))
+        return rc;
+    const tw_chain_buffers &b = *buf;
+    if (!c || !c->x || !c->q || !c->k)
+        return fail(TW_ERR_NULL, "%s: residual stream, q and k buffers required", who);
+    if (!aligned16(c->x) || !aligned16(c->q) || !aligned16(c->k))
+        return fail(TW_ERR_ALIGN, "%s: x, q and k must be 16-byte aligned", who);
+    ChainRange ranges[9];
+    chain_ranges(b, ranges);
+    const struct { const float *p; int64_t w; const char *n; } own[3] = {
+        {c->x, b.hidden, "x"}, {c->q, b.hidden, "q"}, {c->k, b.kv_dim, "k"}};
+    for (int i = 0; i < 3; ++i) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(own[i].p), hi = lo + (uintptr_t)(4 * b.M * own[i].w);
+        if (const char *hit = overlaps_chain(lo, hi, ranges))
+            return fail(TW_ERR_SHAPE, "%s: %s overlaps chain buffer %s", who, own[i].n, hit);
+        for (int j = i + 1; j < 3; ++j) {
+            const uintptr_t l2 = reinterpret_cast<uintptr_t>(own[j].p);
+            if (lo < l2 + (uintptr_t)(4 * b.M * own[j].w) && l2 < hi)
+                return fail(TW_ERR_SHAPE, "%s: %s overlaps %s", who, own[i].n, own[j].n);
+        }
+    }
+    // Every table and every layer's cache is checked before anything is launched.
+    ChainStage st[4];
+    chain_stages(b, st);
+    for (int l = 0; l < n_layers; ++l) {
+        const void *host[4], *dev[4];
+        layer_tables(layers[l], host, dev);
+        for (int s = 0; s < 4; ++s)
+            if (int rc = check_chain_stage(host[s], dev[s], st[s], b.M, l, ranges))
+                return rc;
+        const auto *r = reinterpret_cast<const tw::DescRecord *>(
+            static_cast<const tw::TableHeader *>(host[0]) + 1);
+        if (r[0].y != c->q || r[1].y != c->k)
+            return fail(TW_ERR_SHAPE, "%s: layer %d: q or k does not write its buffer", who, l);
+        tw::RopeAppend ap;
+        tw::PagedAttention at;
+        if (int rc = tw::cached_layer_ops(b, *c, cached[l], &ap, &at))
+            return rc;
+    }
+    const size_t need = tw_chain_workspace_bytes(layers, n_layers);
+    if (!ws || ws_bytes < need)
+        return fail(TW_ERR_BUFSIZE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
+    if (!aligned16(ws))
+        return fail(TW_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+    uint32_t *err = nullptr;
+    if (int rc = err_word(&err))
+        return rc;
+
+    // x = x + y, n = rms(x) * w (y null: the norm alone)
+    auto norm = [&](const float *y, const float *w, float *n) {
+        tw::ResidualNorm a{};
+        a.x = c->x, a.y = y, a.h = y ? c->x : nullptr, a.n = n, a.pre_w = w;
+        a.M = b.M, a.K = b.hidden, a.ldx = a.ldy = a.ldh = a.ldn = b.hidden;
+        a.post = TW_NORM_NONE, a.pre = TW_NORM_RMS, a.alpha = 1.f, a.eps = c->eps;
+        const cudaError_t e = tw::launch_residual_norm(a, stream);
+        return e == cudaSuccess ? TW_OK : cuda_fail(e, "chain norm launch");
+    };
+    int rc = norm(nullptr, cached[0].norm_in, b.h);
+    for (int l = 0; l < n_layers && !rc; ++l) {
+        const void *host[4], *dev[4];
+        layer_tables(layers[l], host, dev);
+        tw::RopeAppend ap;
+        tw::PagedAttention at;
+        if ((rc = tw::cached_layer_ops(b, *c, cached[l], &ap, &at)) ||
+            (rc = tw_decoder_projection_sweep(host[0], dev[0], ws, ws_bytes, stream)))
+            return rc;
+        cudaError_t e = tw::launch_rope_append(ap, err, stream);
+        if (e == cudaSuccess)
+            e = tw::launch_paged_attention(at, err, stream);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "chain attention launch");
+        if ((rc = tw_decoder_projection_sweep(host[1], dev[1], ws, ws_bytes, stream)) ||
+            (rc = norm(b.o, cached[l].norm_mid, b.h1)) ||
+            (rc = tw_decoder_projection_sweep(host[2], dev[2], ws, ws_bytes, stream)))
+            return rc;
+        if ((e = tw::launch_silu_mul(b.g, b.u, b.act, b.M * b.inter, stream)) != cudaSuccess)
+            return cuda_fail(e, "chain SiLU launch");
+        if ((rc = tw_decoder_projection_sweep(host[3], dev[3], ws, ws_bytes, stream)))
+            return rc;
+        rc = norm(b.d, l + 1 < n_layers ? cached[l + 1].norm_in : c->norm_out, b.h);
+    }
+    return rc;
 }
 
 }  // extern "C"

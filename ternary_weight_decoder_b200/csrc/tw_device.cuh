@@ -13,6 +13,7 @@ enum : uint32_t {
     EFLAG_TIMEOUT = 1u,
     EFLAG_NONFINITE = 2u,
     EFLAG_BADDESC = 4u,
+    EFLAG_NOSPACE = 8u,
 };
 
 // Limits handed to every kernel that waits.

@@ -118,6 +118,67 @@ cudaError_t launch_add_f32(const float *x, const float *y, float *out, int64_t n
 cudaError_t launch_silu_mul(const float *g, const float *u, float *out, int64_t n,
                             cudaStream_t stream);
 
+// ------------------------------------------------- paged key-value cache
+// Requests that one assignment handles: their starts, lengths and ranks
+// (16 bytes each) stay in one block's shared memory.
+constexpr int64_t kAssignMaxRequests = 8192;
+struct KvAssign {
+    const int32_t *lengths, *delta;
+    int32_t *block_table, *free_pages;
+    const int32_t *free_count;
+    int32_t *lengths_out, *free_count_out;
+    int32_t *slots, *positions, *request_of_row;  // [rows]
+    int32_t *row_start;                           // [requests + 1], or null
+    int64_t requests, page_size, max_pages, table_stride, free_capacity, rows;
+};
+cudaError_t launch_kv_assign(const KvAssign &a, uint32_t *err, cudaStream_t stream);
+
+struct RopeAppend {
+    const float *q, *k, *v;
+    float *q_out;
+    int64_t ldq, ldk, ldv, ldqo;
+    const int32_t *positions, *slots;
+    const double *inv_freq;
+    int64_t rows;
+    int heads, kv_heads, head_dim, rotary, interleaved;
+    tw_kv_cache cache;
+};
+cudaError_t launch_rope_append(const RopeAppend &a, uint32_t *err, cudaStream_t stream);
+
+struct PagedAttention {
+    const float *q;
+    float *out, *lse;              // lse may be null
+    int64_t ldq, ldo;
+    const int32_t *block_table, *lengths, *first;  // first may be null
+    int64_t requests, max_pages, table_stride;
+    int heads;
+    float scale;
+    tw_kv_cache cache;
+    uint8_t *ws;
+};
+int64_t paged_attention_ws_bytes(int64_t requests, int64_t heads, int64_t kv_heads, int64_t head_dim);
+cudaError_t launch_paged_attention(const PagedAttention &a, uint32_t *err, cudaStream_t stream);
+
+// ------------------------------------------------------- residual and norms
+constexpr int64_t kNormMaxK = 32768;
+struct ResidualNorm {
+    const float *x, *y;            // y may be null: h = x
+    const float *post_w, *post_b, *gate, *pre_w, *pre_b;
+    float *h, *n;                  // either may be null
+    int8_t *xq;
+    float *amax;
+    int32_t *qsum;
+    int64_t M, K, ldx, ldy, ldg, ldh, ldn;   // ldg 0: one gate row for all
+    int post, pre;                 // TW_NORM_*
+    float alpha, eps;
+};
+cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream);
+
+// The append and the attention of one layer of tw_decoder_chain_cached, checked
+// (TW_OK or a status with its message).
+int cached_layer_ops(const tw_chain_buffers &b, const tw_chain_cache &c, const tw_cached_layer &L,
+                     RopeAppend *append, PagedAttention *attention);
+
 // ------------------------------------------------------------ launchers
 // Each returns a cudaError_t from the launch.
 cudaError_t launch_ternarize(const float *W, int64_t N, int64_t K, uint8_t *packed,
