@@ -115,7 +115,7 @@ int check_attention(const tw::PagedAttention &p, size_t ws_bytes, const char *wh
     if (overlap(p.q, 4 * ((p.requests - 1) * p.ldq + p.heads * D), p.out,
                 4 * ((p.requests - 1) * p.ldo + p.heads * D)))
         return fail(TW_ERR_SHAPE, "%s: out overlaps q", who);
-    const size_t need = (size_t)tw::paged_attention_ws_bytes(p.requests, p.heads, p.cache.kv_heads, D);
+    const size_t need = (size_t)tw::paged_attention_ws_bytes(D);
     if (!p.ws || ws_bytes < need)
         return fail(TW_ERR_BUFSIZE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
     if (!aligned(p.ws, 16))
@@ -252,7 +252,7 @@ size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads, int64
     if (requests < 1 || requests > (1 << 24) || heads < 1 || heads > 65536 || kv_heads < 1 ||
         heads % kv_heads || head_dim < 8 || head_dim > 256)
         return 0;
-    return (size_t)tw::paged_attention_ws_bytes(requests, heads, kv_heads, head_dim);
+    return (size_t)tw::paged_attention_ws_bytes(head_dim);
 }
 
 int tw_paged_attention(const float *q, int64_t ldq, int64_t requests, int64_t heads,

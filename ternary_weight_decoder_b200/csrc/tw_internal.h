@@ -156,7 +156,7 @@ struct PagedAttention {
     tw_kv_cache cache;
     uint8_t *ws;
 };
-int64_t paged_attention_ws_bytes(int64_t requests, int64_t heads, int64_t kv_heads, int64_t head_dim);
+int64_t paged_attention_ws_bytes(int64_t head_dim);
 cudaError_t launch_paged_attention(const PagedAttention &a, uint32_t *err, cudaStream_t stream);
 
 // ------------------------------------------------------- residual and norms
