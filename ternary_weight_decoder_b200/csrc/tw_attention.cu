@@ -7,56 +7,71 @@
 //
 // Bound by memory: every visible key and value is read once, and each element
 // serves the few query heads of its group only (2 * heads / kv_heads
-// multiply-adds per element and head), far below what tcgen05 tiles of 128
-// rows need to pay; mma.sync tiles of 16 x 8 keep up with the memory at a
-// fraction of their rate.
+// multiply-adds per element), far below what tcgen05 tiles of 128 rows need
+// to pay; mma.sync tiles keep up with the memory at a fraction of their rate.
 //
-// Split: the keys of all requests and KV heads are cut into tiles of 64, laid
-// end to end, and every block takes an equal run of them, whatever the
-// lengths are.  A block whose run holds all of a (request, KV head) writes its
-// output; the pieces of one that spans blocks go to the workspace, and the
-// block that finishes last joins them in a fixed order.  Inside a block each
-// of four warps takes 16 keys of every tile through its own ring of
-// cp.async stages: no barrier until a piece ends.
+// Split: the keys of all requests and KV heads are cut into tiles, laid end
+// to end, and every block takes an equal run of them, whatever the lengths
+// are.  A block whose run holds all of a (request, KV head) writes its
+// output; the pieces of one that spans blocks go to the workspace and are
+// joined in a fixed order, by the last block of every sixteen and then by the
+// last of those.  Inside a block each warp takes 16 keys of every tile
+// through its own ring of cp.async stages: no barrier until a piece ends.
 //
-// Eight query heads ride in one 16-row MMA operand together with what their
-// first rounding left over: rows 0-7 hold the operand rounded to the cache's
-// type, rows 8-15 the remainder, so that queries and weights are carried in 22
-// bits (fp16) at no extra instruction.  bf16's eight bits need a third part,
-// in a second MMA.  Larger groups are split into units of eight heads.
+// Matrix products: the 16 keys (or 16 columns of the values) are the rows of
+// an MMA, eight query heads its columns, so no lane computes for nobody:
+// scores^T = K q^T, out^T = V^T w^T.  The operands that are not in the cache
+// are carried in parts, each the rounding of what the last one left: two of
+// fp16 (22 bits), three of bf16 (24 bits), the scores and sums in fp32.
+// Groups of more than eight heads are split into units of eight.
 #include <cfloat>
 
 #include "tw_kv.cuh"
 
+#ifndef TW_ATT_WARPS
+#define TW_ATT_WARPS 8
+#endif
+#ifndef TW_ATT_BLOCKS
+#define TW_ATT_BLOCKS 1
+#endif
+#ifndef TW_ATT_QS
+#define TW_ATT_QS 0
+#endif
+
 namespace tw {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 16;                    // keys of a warp's step
-constexpr int kTile = kKeys * kWarps;
 constexpr int kMaxCtas = 512;                // counters and partial results in the workspace
 constexpr int kHeads = 8;                    // query heads of a unit
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kFan = 16;                     // pieces that one block joins
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 // The shape of one variant: DP columns (head_dim rounded up) of type DT.
 template <int DT, int DP>
 struct Shape {
     static constexpr bool kCodes = DT == TW_KV_I8;
-    static constexpr bool kThird = DT == TW_KV_BF16;   // a third part of queries and weights
+    static constexpr bool kBf = DT == TW_KV_BF16;
+    static constexpr int kParts = kBf ? 3 : 2;         // of queries and weights
     static constexpr int kElem = kCodes ? 1 : 2;
     static constexpr int kRow = DP * kElem;            // bytes of a key
     static constexpr int kChunks = kRow / 16;
     static constexpr int kPool = kKeys * kRow;         // bytes of a step's keys
     static constexpr int kStage = 2 * kPool + (kCodes ? 2 * kKeys * 4 : 0);
     static constexpr int kSteps = DP / 16;             // MMA steps over the columns
-    static constexpr int kTiles = DP / 8;              // MMA tiles of output columns
-    // Queries in registers up to 128 columns, in shared memory above (the
-    // accumulators take half of the registers there).
-    static constexpr bool kQueryShared = DP > 128;
-    static constexpr int kQueryBytes = kQueryShared ? kSteps * 32 * (kThird ? 24 : 16) : 0;
-    static constexpr int kStages = DP == 256 ? (kCodes ? 5 : 3) : DP == 128 ? (kCodes ? 5 : 3) : (kCodes ? 8 : 6);
+    static constexpr int kWarps = DP > 128 ? TW_ATT_WARPS / 2 : TW_ATT_WARPS;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kTile = kKeys * kWarps;
+    static constexpr int kBlocks = TW_ATT_BLOCKS;      // resident on an SM
+    // Queries in registers up to 128 columns, in shared memory above.
+    static constexpr bool kQueryShared = DP > 128 || TW_ATT_QS;
+    static constexpr int kQueryBytes = kQueryShared ? kSteps * 32 * 8 * kParts : 0;
+    static constexpr int kRoom = (227 * 1024) / kBlocks - 2048 - kQueryBytes;
+    static constexpr int kFit = kRoom / (kWarps * kStage);
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kWarps * kStages * kStage + kQueryBytes;
+    static_assert(kStages >= 2, "two stages at least");
+    static_assert(kHeads * DP * 4 <= kStage, "a stage holds a warp's sums");
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -129,24 +144,36 @@ __device__ __forceinline__ uint32_t split2(float &x, float &y)
     return bits;
 }
 
-// Two bytes of w ^ 0x80808080 (the codes plus 128) as exact fp16 codes: a
-// byte b under the exponent of 1024 is 1024 + b, less 1152 the code.
-template <int SEL>
+// Bytes 0 and 2 of w, or 1 and 3, as exact fp16 codes: a code plus 128 under
+// the exponent of 1024 is 1152 + code.
+template <bool ODD>
 __device__ __forceinline__ uint32_t codes2(uint32_t w)
 {
-    const uint32_t h = __byte_perm(w, 0x64646464u, SEL);
+    const uint32_t h = ((ODD ? w >> 8 : w) & 0x00ff00ffu) ^ 0x64806480u;
     const uint32_t off = 0x64806480u;   // 1152 twice
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&off));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 
+// The 8 x 8 matrix of 16-bit values whose rows the lanes' quads hold, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // Byte offset of 16-byte chunk c of key row in a step's pool: chunks are
 // permuted by the row so that eight rows of one chunk fall on all banks.
 template <int CHUNKS>
+__device__ __forceinline__ int row_swap(int row)
+{
+    return CHUNKS >= 8 ? (row & 7) : ((row >> 1) & 3);
+}
+template <int CHUNKS>
 __device__ __forceinline__ uint32_t place(int row, int c)
 {
-    const int x = CHUNKS >= 8 ? (row & 7) : ((row >> 1) & 3);
-    return (uint32_t)(row * CHUNKS + (c ^ x)) * 16;
+    return (uint32_t)(row * CHUNKS + (c ^ row_swap<CHUNKS>(row))) * 16;
 }
 
 // The visible keys of a request, as tiles.
@@ -154,6 +181,7 @@ struct Span {
     int lo, hi, first_tile, tiles;
 };
 
+template <int TILE>
 __device__ __forceinline__ Span span_of(const PagedAttention &a, int64_t r, bool report, uint32_t *err)
 {
     Span s;
@@ -166,12 +194,13 @@ __device__ __forceinline__ Span span_of(const PagedAttention &a, int64_t r, bool
     }
     s.hi = (int)hi;
     s.lo = a.first ? max(a.first[r], 0) : 0;
-    s.first_tile = s.lo / kTile;
-    s.tiles = s.hi > s.lo ? (s.hi - 1) / kTile + 1 - s.first_tile : 0;
+    s.first_tile = s.lo / TILE;
+    s.tiles = s.hi > s.lo ? (s.hi - 1) / TILE + 1 - s.first_tile : 0;
     return s;
 }
 
 // A place in the run of tiles: tile t of unit u of request r.
+template <int TILE>
 struct Cursor {
     int64_t r;
     int u, t;
@@ -188,7 +217,7 @@ struct Cursor {
             ++r;
             if (r >= a.requests)
                 return;
-            s = span_of(a, r, false, nullptr);
+            s = span_of<TILE>(a, r, false, nullptr);
         } while (s.tiles == 0);
     }
 };
@@ -204,18 +233,65 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane)
     return v;
 }
 
+// The pieces of one unit in the workspace: maxima and sums [piece][head][2],
+// sums of values [piece][head][DP].
+template <int DP>
+struct Pieces {
+    float *ml, *o;
+    __device__ __forceinline__ float *at_ml(int64_t piece, int h) const { return ml + (piece * kHeads + h) * 2; }
+    __device__ __forceinline__ float *at_o(int64_t piece, int h) const { return o + (piece * kHeads + h) * DP; }
+};
+
+// Join `count` <= 32 pieces of head h, piece i being piece_of(i), by one
+// warp, in the order of i.  Columns 4 * lane + 128 q of the sum stay in x.
+template <int DP, class F>
+__device__ __forceinline__ void join(const Pieces<DP> &w, int count, int h, F piece_of,
+                                     float4 (&x)[DP > 128 ? 2 : 1], float &top, float &sum)
+{
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f;
+    if (lane < count) {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(w.at_ml(piece_of(lane), h)));
+        m = v.x, l = v.y;
+    }
+    top = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = m == -INFINITY ? 0.f : ex2(m - top);
+    sum = l * f;   // (a piece without a maximum can hold a NaN sum: it stays one)
+    if (l != l)
+        sum = l;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
+        x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int c = min(4 * lane + 128 * q, DP - 4);
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(w.at_o(piece_of(i), h) + c));
+            const float g = __shfl_sync(0xffffffffu, f, i);
+            x[q].x = fmaf(y.x, g, x[q].x), x[q].y = fmaf(y.y, g, x[q].y);
+            x[q].z = fmaf(y.z, g, x[q].z), x[q].w = fmaf(y.w, g, x[q].w);
+        }
+    }
+}
+
 template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAttention a, uint32_t *err)
+__global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlocks)
+    k_paged_attention(const PagedAttention a, uint32_t *err)
 {
     using S = Shape<DT, DP>;
-    constexpr bool BF = DT == TW_KV_BF16;
+    constexpr bool BF = S::kBf;
+    constexpr int W = S::kWarps, kThreads = S::kThreads, kTile = S::kTile;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t part[kWarps];
+    __shared__ int64_t part[W];
     __shared__ int64_t start_r;
-    __shared__ int start_u, start_t;
-    __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
-    __shared__ uint32_t sm_mask[kWarps][S::kStages];
-    __shared__ int last;
+    __shared__ int start_u, start_t, last;
+    __shared__ float sm_m[W][kHeads], sm_l[W][kHeads];
+    __shared__ uint32_t sm_mask[W][S::kStages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int D = (int)a.cache.head_dim, P = (int)a.cache.page_size, kvh = (int)a.cache.kv_heads;
     const int group = a.heads / kvh, per_kv = (group + kHeads - 1) / kHeads, units = kvh * per_kv;
@@ -226,14 +302,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
     const int64_t rlo = min((int64_t)tid * per, R), rhi = min(rlo + per, R);
     int64_t sum = 0;
     for (int64_t r = rlo; r < rhi; ++r)
-        sum += span_of(a, r, blockIdx.x == 0, err).tiles;
+        sum += span_of<kTile>(a, r, blockIdx.x == 0, err).tiles;
     const int64_t incl = warp_inclusive(sum, lane);
     if (lane == 31)
         part[warp] = incl;
     __syncthreads();
     int64_t before = incl - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
         before += w < warp ? part[w] : 0;
         total += part[w];
     }
@@ -244,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
     if (begin < end && before * units <= begin && begin < (before + sum) * units) {
         int64_t at = before * units, r = rlo;
         for (;; ++r) {
-            const int64_t n = (int64_t)span_of(a, r, false, nullptr).tiles * units;
+            const int64_t n = (int64_t)span_of<kTile>(a, r, false, nullptr).tiles * units;
             if (begin < at + n) {
                 const int64_t tiles = n / units;
                 start_r = r;
@@ -257,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
     }
     // rows without keys
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-        if (span_of(a, r, false, nullptr).tiles)
+        if (span_of<kTile>(a, r, false, nullptr).tiles)
             continue;
         for (int c = tid; c < a.heads * D; c += kThreads)
             a.out[r * a.ldo + c] = 0.f;
@@ -268,24 +344,59 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
     __syncthreads();
     if (begin >= end)
         return;
-    Cursor load, use;
+    Cursor<kTile> load, use;
     load.r = start_r, load.u = start_u, load.t = start_t;
-    load.s = span_of(a, load.r, false, nullptr);
+    load.s = span_of<kTile>(a, load.r, false, nullptr);
     use = load;
 
     // ---- the ring of stages
+    constexpr int kRowsPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;   // rows of one pass of the warp
     const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
-    const uint8_t *kpool = static_cast<const uint8_t *>(a.cache.k);
-    const uint8_t *vpool = static_cast<const uint8_t *>(a.cache.v);
-    const int row_chunks = D * S::kElem / 16;
+    const int row0 = lane / S::kChunks, chunk = lane % S::kChunks;
+    const uint32_t lane_dst = place<S::kChunks>(row0, chunk);
+    const int64_t row_bytes = a.cache.token_stride * S::kElem;
+    const uint8_t *kpool = static_cast<const uint8_t *>(a.cache.k) + row0 * row_bytes + chunk * 16;
+    const uint8_t *vpool = static_cast<const uint8_t *>(a.cache.v) + row0 * row_bytes + chunk * 16;
+    const bool in_row = chunk < D * S::kElem / 16;
+    const bool page_steps = P % kKeys == 0;   // the 16 keys of a step share a page
+    const int page_shift = (P & (P - 1)) == 0 ? __ffs(P) - 1 : -1;
     auto fetch = [&](int stage) {
         const int head = load.u / per_kv;
-        const int j = (load.s.first_tile + load.t) * kTile + warp * kKeys + (lane & 15);
+        const int j0 = (load.s.first_tile + load.t) * kTile + warp * kKeys;
+        const uint32_t base = ring + stage * S::kStage;
+        const int32_t *table = a.block_table + load.r * a.table_stride;
+        if (page_steps && j0 >= load.s.lo && j0 + kKeys <= load.s.hi) {
+            const int p = page_shift >= 0 ? j0 >> page_shift : j0 / P;
+            const int page = __ldg(table + p);
+            if ((uint32_t)page < (uint32_t)a.cache.num_pages) {
+                const int in = j0 - p * P;
+                const int64_t off = (page * a.cache.page_stride + in * a.cache.token_stride +
+                                     head * a.cache.head_stride) * S::kElem;
+                const uint8_t *ks = kpool + off, *vs = vpool + off;
+#pragma unroll
+                for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                    const uint32_t dst = base + (lane_dst ^ (row_swap<S::kChunks>(kRowsPer * i) << 4)) +
+                                         kRowsPer * i * S::kRow;
+                    cp_async16(dst, in_row ? ks : kpool, in_row);
+                    cp_async16(dst + S::kPool, in_row ? vs : kpool, in_row);
+                    ks += kRowsPer * row_bytes, vs += kRowsPer * row_bytes;
+                }
+                if (S::kCodes) {
+                    const int64_t slot = ((int64_t)page * P + in + (lane & 15)) * kvh + head;
+                    cp_async4(base + 2 * S::kPool + lane * 4,
+                              (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + slot, true);
+                }
+                if (lane == 0)
+                    sm_mask[warp][stage] = 0xffffu;
+                return;
+            }
+        }
+        const int j = j0 + (lane & 15);
         bool ok = j >= load.s.lo && j < load.s.hi;
         int64_t off = 0, slot = 0;
         if (ok) {
             const int p = j / P;
-            const int page = __ldg(a.block_table + load.r * a.table_stride + p);
+            const int page = __ldg(table + p);
             if ((uint32_t)page < (uint32_t)a.cache.num_pages) {
                 const int in = j - p * P;
                 off = (page * a.cache.page_stride + in * a.cache.token_stride + head * a.cache.head_stride) *
@@ -299,24 +410,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
         const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
         if (lane == 0)
             sm_mask[warp][stage] = mask;
-        const uint32_t base = ring + stage * S::kStage;
-#pragma unroll
-        for (int i = 0; i < S::kChunks / 2; ++i) {
-            const int idx = i * 32 + lane, row = idx / S::kChunks, c = idx % S::kChunks;
-            const int64_t o = __shfl_sync(0xffffffffu, off, row) + c * 16;
-            const bool in = ((mask >> row) & 1) && c < row_chunks;
-            const uint32_t dst = base + place<S::kChunks>(row, c);
-            cp_async16(dst, kpool + (in ? o : 0), in);
-            cp_async16(dst + S::kPool, vpool + (in ? o : 0), in);
+#pragma unroll 1
+        for (int i = 0; i < kKeys / kRowsPer; ++i) {
+            const int row = row0 + kRowsPer * i;
+            const int64_t o = __shfl_sync(0xffffffffu, off, row) - row0 * row_bytes;
+            const bool in = ((mask >> row) & 1) && in_row;
+            const uint32_t dst = base + place<S::kChunks>(row, chunk);
+            cp_async16(dst, in ? kpool + o : a.cache.k, in);
+            cp_async16(dst + S::kPool, in ? vpool + o : a.cache.v, in);
         }
-        if (S::kCodes) {
-            const float *src = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
-            cp_async4(base + 2 * S::kPool + lane * 4, src + (ok ? slot : 0), ok);
-        }
+        if (S::kCodes)
+            cp_async4(base + 2 * S::kPool + lane * 4,
+                      (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + (ok ? slot : 0), ok);
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-    const int64_t n = end - begin;
+    const int n = (int)(end - begin);
 #pragma unroll 1
     for (int s = 0; s < S::kStages - 1; ++s) {
         if (s < n) {
@@ -326,31 +435,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
         commit();
     }
 
-    uint32_t qa[S::kQueryShared ? 1 : S::kSteps][4], qb[S::kQueryShared || !S::kThird ? 1 : S::kSteps][2];
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + kWarps * S::kStages * S::kStage);
-    uint2 *qs3 = reinterpret_cast<uint2 *>(qs + S::kSteps * 32);
-    float o[S::kTiles][4], m = -INFINITY, l = 0.f, unscale = 1.f;
+    // Queries as the MMA's B operand, in parts: [step][part] the pairs of
+    // columns (head g of the unit) that this lane feeds.
+    constexpr int kQ = S::kQueryShared ? 1 : S::kSteps;
+    uint32_t qb[kQ][S::kParts][2];
+    uint2 *qs = reinterpret_cast<uint2 *>(smem + W * S::kStages * S::kStage);
+    float o[S::kSteps][4];           // (columns g, g + 8 of 16) x (heads 2 t4, 2 t4 + 1)
+    float m[2], l[2], unscale[2];    // of heads 2 t4, 2 t4 + 1
     int stage = 0;
     bool fresh = true;
 #pragma unroll 1
-    for (int64_t i = 0; i < n; ++i) {
+    for (int i = 0; i < n; ++i) {
         // ---- a new piece: its queries, split
         if (fresh) {
             const int h0 = (use.u / per_kv) * group + (use.u % per_kv) * kHeads;
             const bool live = (use.u % per_kv) * kHeads + g < group;
             const float *row = a.q + use.r * a.ldq + (int64_t)(h0 + (live ? g : 0)) * D;
             const float mul = a.scale * kLog2e;
-            // columns of step j that this lane holds: two pairs, 16 bytes apart
-            // in a 16-bit row; four in a row where the row holds codes
+            // columns of step j that this lane holds.  Codes: four in a row,
+            // even and odd ones apart, as codes2 takes them out of a word.
             auto load4 = [&](int j, float (&x)[4]) {
                 const int c0 = S::kCodes ? 16 * j + 4 * t4 : 16 * j + 2 * t4;
                 const int c1 = S::kCodes ? c0 + 2 : c0 + 8;
                 const float2 p = live && c0 < D ? *reinterpret_cast<const float2 *>(row + c0) : make_float2(0.f, 0.f);
                 const float2 q = live && c1 < D ? *reinterpret_cast<const float2 *>(row + c1) : make_float2(0.f, 0.f);
-                x[0] = p.x * mul, x[1] = p.y * mul, x[2] = q.x * mul, x[3] = q.y * mul;
+                x[0] = p.x * mul, x[1] = (S::kCodes ? q.x : p.y) * mul;
+                x[2] = (S::kCodes ? p.y : q.x) * mul, x[3] = q.y * mul;
             };
-            float norm = 1.f;
-            unscale = 1.f;
+            float norm = 1.f, back = 1.f;
             if (!BF) {
                 // fp16 operands: the head's largest query is brought to 2^14
                 // by a power of two, so that neither part leaves the range
@@ -364,48 +476,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-                norm = top > 0.f && top <= FLT_MAX ? __uint_as_float((uint32_t)(127 + 14 - e) << 23) : 1.f;
-                unscale = top > 0.f && top <= FLT_MAX ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.f;
+                const bool some = top > 0.f && top <= FLT_MAX;
+                norm = some ? __uint_as_float((uint32_t)(127 + 14 - e) << 23) : 1.f;
+                back = some ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.f;
             }
-            if (S::kQueryShared)
-                __syncthreads();   // the last piece's queries are read
+            unscale[0] = __shfl_sync(0xffffffffu, back, 8 * t4);
+            unscale[1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
 #pragma unroll
             for (int j = 0; j < S::kSteps; ++j) {
-                if (S::kQueryShared && (j & (kWarps - 1)) != warp)
+                if (S::kQueryShared && j % W != warp)
                     continue;
                 float x[4];
                 load4(j, x);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     x[k] *= norm;
-                uint32_t w[4], w3[2];
-                w[0] = split2<BF>(x[0], x[1]);
-                w[2] = split2<BF>(x[2], x[3]);
-                w[1] = split2<BF>(x[0], x[1]);
-                w[3] = split2<BF>(x[2], x[3]);
-                if (S::kThird) {
-                    w3[0] = split2<BF>(x[0], x[1]);
-                    w3[1] = split2<BF>(x[2], x[3]);
-                }
-                if (S::kQueryShared) {
-                    qs[j * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (S::kThird)
-                        qs3[j * 32 + lane] = make_uint2(w3[0], w3[1]);
-                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        qa[S::kQueryShared ? 0 : j][k] = w[k];
-                    if (S::kThird) {
-                        qb[S::kQueryShared ? 0 : j][0] = w3[0];
-                        qb[S::kQueryShared ? 0 : j][1] = w3[1];
-                    }
+                for (int k = 0; k < S::kParts; ++k) {
+                    const uint32_t b0 = split2<BF>(x[0], x[1]), b1 = split2<BF>(x[2], x[3]);
+                    if (S::kQueryShared)
+                        qs[(j * S::kParts + k) * 32 + lane] = make_uint2(b0, b1);
+                    else
+                        qb[S::kQueryShared ? 0 : j][k][0] = b0, qb[S::kQueryShared ? 0 : j][k][1] = b1;
                 }
             }
             if (S::kQueryShared)
                 __syncthreads();
-            m = -INFINITY, l = 0.f;
+            m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
 #pragma unroll
-            for (int c = 0; c < S::kTiles; ++c)
+            for (int c = 0; c < S::kSteps; ++c)
                 o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
             fresh = false;
         }
@@ -421,141 +520,125 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
         const uint32_t kbase = ring + stage * S::kStage, vbase = kbase + S::kPool;
         const uint32_t mask = sm_mask[warp][stage];
         if (mask) {
-            // ---- scores: heads g x keys 8 k + 2 t4 + {0, 1}
-            float acc[2][4] = {}, third[2][4] = {};
-            auto score_step = [&](int j, const uint32_t (&b)[2][2]) {
-                uint32_t w[4], w3[2] = {0, 0};
-                if (S::kQueryShared) {
-                    const uint4 v = qs[j * 32 + lane];
-                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                    if (S::kThird) {
-                        const uint2 v3 = qs3[j * 32 + lane];
-                        w3[0] = v3.x, w3[1] = v3.y;
+            // ---- scores of keys g, g + 8 for heads 2 t4, 2 t4 + 1
+            float acc[S::kParts][4] = {};
+            auto score = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int k = 0; k < S::kParts; ++k) {
+                    uint32_t b0, b1;
+                    if (S::kQueryShared) {
+                        const uint2 v = qs[(j * S::kParts + k) * 32 + lane];
+                        b0 = v.x, b1 = v.y;
+                    } else {
+                        b0 = qb[S::kQueryShared ? 0 : j][k][0], b1 = qb[S::kQueryShared ? 0 : j][k][1];
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = qa[S::kQueryShared ? 0 : j][k];
-                    if (S::kThird)
-                        w3[0] = qb[S::kQueryShared ? 0 : j][0], w3[1] = qb[S::kQueryShared ? 0 : j][1];
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    mma<BF>(acc[k], w[0], w[1], w[2], w[3], b[k][0], b[k][1]);
-                    if (S::kThird)
-                        mma<BF>(third[k], w3[0], 0u, w3[1], 0u, b[k][0], b[k][1]);
+                    mma<BF>(acc[k], a0, a1, a2, a3, b0, b1);
                 }
             };
             if (S::kCodes) {
 #pragma unroll
                 for (int j = 0; j < S::kSteps; j += 2) {
-                    uint32_t f[4];
-                    ldmatrix4<false>(f, kbase + place<S::kChunks>((lane & 7) + (lane & 8), j + (lane >> 4)));
-                    uint32_t b[2][2];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t x = f[2 * s + k] ^ 0x80808080u;
-                            b[k][0] = codes2<0x4140>(x);
-                            b[k][1] = codes2<0x4342>(x);
-                        }
-                        score_step(j + s, b);
-                    }
+                    uint32_t f[4];   // (keys 0-7, 8-15) x (chunks j, j + 1)
+                    ldmatrix4<false>(f, kbase + place<S::kChunks>(lane & 15, j + (lane >> 4)));
+                    score(j, codes2<false>(f[0]), codes2<false>(f[1]), codes2<true>(f[0]), codes2<true>(f[1]));
+                    score(j + 1, codes2<false>(f[2]), codes2<false>(f[3]), codes2<true>(f[2]), codes2<true>(f[3]));
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < S::kSteps; ++j) {
                     uint32_t f[4];
-                    ldmatrix4<false>(f, kbase + place<S::kChunks>((lane & 7) + ((lane >> 4) << 3),
-                                                                   2 * j + ((lane >> 3) & 1)));
-                    const uint32_t b[2][2] = {{f[0], f[1]}, {f[2], f[3]}};
-                    score_step(j, b);
+                    ldmatrix4<false>(f, kbase + place<S::kChunks>(lane & 15, 2 * j + (lane >> 4)));
+                    score(j, f[0], f[1], f[2], f[3]);
                 }
             }
             // ---- running maximum and sum.  With codes the value's scale goes
             // into the weight (as its logarithm, so that weights stay within
             // fp16 whatever the scales are): w_j = 2^(s_j + log2 vs_j - m).
-            float s[2][2], lv[2][2], top = -INFINITY;
+            float s[4], lv[2] = {0.f, 0.f}, ks[2] = {1.f, 1.f};
+            if (S::kCodes) {
+                const float *sc = reinterpret_cast<const float *>(
+                    smem + (warp * S::kStages + stage) * S::kStage + 2 * S::kPool);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int key = 8 * k + 2 * t4 + e;
-                    float x = acc[k][e] + acc[k][2 + e];
-                    if (S::kThird)
-                        x += third[k][e];
-                    lv[k][e] = 0.f;
-                    if (S::kCodes) {
-                        const float *sc = reinterpret_cast<const float *>(
-                            smem + (warp * S::kStages + stage) * S::kStage + 2 * S::kPool);
-                        x *= unscale * sc[key];
-                        const float vs = sc[kKeys + key];
-                        lv[k][e] = vs > 0.f ? log2f(vs) : 0.f;
-                    } else if (!BF) {
-                        x *= unscale;
-                    }
-                    s[k][e] = (mask >> key) & 1 ? x : -INFINITY;
-                    top = fmaxf(top, s[k][e] + lv[k][e]);
+                for (int k = 0; k < 2; ++k) {
+                    ks[k] = sc[g + 8 * k];
+                    const float vs = sc[kKeys + g + 8 * k];
+                    lv[k] = vs > 0.f ? __log2f(vs) : 0.f;
                 }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (__any_sync(0xffffffffu, top > m)) {
-                const float up = fmaxf(top, m);
-                const float f = up == -INFINITY ? 1.f : ex2(m - up);
-                m = up;
-                l *= f;
+            }
 #pragma unroll
-                for (int c = 0; c < S::kTiles; ++c)
+            for (int e = 0; e < 4; ++e) {
+                float x = acc[0][e] + acc[1][e];
+                if (S::kParts == 3)
+                    x += acc[S::kParts - 1][e];
+                if (!BF)
+                    x *= unscale[e & 1];
+                if (S::kCodes)
+                    x *= ks[e >> 1];
+                s[e] = (mask >> (g + 8 * (e >> 1))) & 1 ? x : -INFINITY;
+            }
+            float top[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                top[h] = S::kCodes ? fmaxf(s[h] + lv[0], s[2 + h] + lv[1]) : fmaxf(s[h], s[2 + h]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+            if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+                float f[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float up = fmaxf(top[h], m[h]);
+                    f[h] = up == -INFINITY ? 1.f : ex2(m[h] - up);
+                    m[h] = up;
+                    l[h] *= f[h];
+                }
+#pragma unroll
+                for (int c = 0; c < S::kSteps; ++c)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        o[c][e] *= f;
+                        o[c][e] *= f[e & 1];
             }
             // fp16 weights are carried times 2^14 (as is the sum), so that
             // the second part of small ones stays clear of fp16's smallest
-            const float shift = (m == -INFINITY ? 0.f : m) - (BF ? 0.f : 14.f);
-            float p[2][2];
+            float p[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    p[k][e] = ex2(s[k][e] + lv[k][e] - shift);
-                    l += S::kCodes ? ex2(s[k][e] - shift) : p[k][e];
-                }
-            uint32_t w[4], w3[2] = {0, 0};
-            w[0] = split2<BF>(p[0][0], p[0][1]);
-            w[2] = split2<BF>(p[1][0], p[1][1]);
-            w[1] = split2<BF>(p[0][0], p[0][1]);
-            w[3] = split2<BF>(p[1][0], p[1][1]);
-            if (S::kThird) {
-                w3[0] = split2<BF>(p[0][0], p[0][1]);
-                w3[1] = split2<BF>(p[1][0], p[1][1]);
+            for (int e = 0; e < 4; ++e) {
+                const float shift = (m[e & 1] == -INFINITY ? 0.f : m[e & 1]) - (BF ? 0.f : 14.f);
+                const float x = s[e] - shift;
+                p[e] = ex2(S::kCodes ? x + lv[e >> 1] : x);
+                l[e & 1] += S::kCodes ? ex2(x) : p[e];
             }
-            // ---- weighted values
-            if (S::kCodes) {
-                // a transposed 8 x 8 matrix of byte pairs: keys 2 t4 + {0, 1}, columns 2 g + {0, 1}
+            uint32_t w[S::kParts][2];
 #pragma unroll
-                for (int c = 0; c < S::kChunks; c += 2) {
-                    uint32_t f[4];
-                    ldmatrix4<true>(f, vbase + place<S::kChunks>((lane & 7) + (lane & 8), c + (lane >> 4)));
+            for (int k = 0; k < S::kParts; ++k) {
+                w[k][0] = transpose8(split2<BF>(p[0], p[1]));
+                w[k][1] = transpose8(split2<BF>(p[2], p[3]));
+            }
+            // ---- weighted values: columns x heads
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t x0 = f[2 * q] ^ 0x80808080u, x1 = f[2 * q + 1] ^ 0x80808080u;
-                        mma<false>(o[2 * (c + q)], w[0], w[1], w[2], w[3], codes2<0x4240>(x0), codes2<0x4240>(x1));
-                        mma<false>(o[2 * (c + q) + 1], w[0], w[1], w[2], w[3], codes2<0x4341>(x0), codes2<0x4341>(x1));
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < S::kTiles; c += 2) {
-                    uint32_t f[4];
-                    ldmatrix4<true>(f, vbase + place<S::kChunks>((lane & 7) + (lane & 8), c + (lane >> 4)));
+            for (int c = 0; c < S::kSteps; c += S::kCodes ? 2 : 1) {
+                uint32_t f[4];
+                if (S::kCodes) {
+                    // byte pairs: keys 2 t4 + {0, 1}, columns 2 g + {0, 1} of
+                    // chunks c, c + 1; even columns are rows 0-7, odd ones 8-15
+                    ldmatrix4<true>(f, vbase + place<S::kChunks>(lane & 15, c + (lane >> 4)));
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        mma<BF>(o[c + q], w[0], w[1], w[2], w[3], f[2 * q], f[2 * q + 1]);
-                        if (S::kThird)
-                            mma<BF>(o[c + q], w3[0], 0u, w3[1], 0u, f[2 * q], f[2 * q + 1]);
+                        const uint32_t a0 = codes2<false>(f[2 * q]), a1 = codes2<true>(f[2 * q]);
+                        const uint32_t a2 = codes2<false>(f[2 * q + 1]), a3 = codes2<true>(f[2 * q + 1]);
+#pragma unroll
+                        for (int k = 0; k < S::kParts; ++k)
+                            mma<BF>(o[S::kCodes ? c + q : c], a0, a1, a2, a3, w[k][0], w[k][1]);
                     }
+                } else {
+                    // (columns 0-7, 8-15) x (keys 0-7, 8-15)
+                    ldmatrix4<true>(f, vbase + place<S::kChunks>((lane & 7) + ((lane >> 4) << 3),
+                                                                  2 * c + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int k = 0; k < S::kParts; ++k)
+                        mma<BF>(o[c], f[0], f[1], f[2], f[3], w[k][0], w[k][1]);
                 }
             }
         }
@@ -566,119 +649,124 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention(const PagedAtte
             const int64_t ubeg = begin + i - use.t, uend = ubeg + use.s.tiles;
             const int h0 = (use.u / per_kv) * group + (use.u % per_kv) * kHeads;
             const int heads = min(kHeads, group - (use.u % per_kv) * kHeads);
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
             __syncwarp();   // the stage is read: it takes the warp's sums
             float *mine = reinterpret_cast<float *>(smem + (warp * S::kStages + stage) * S::kStage);
             // [head][column], columns permuted by the head against bank conflicts
-            auto at = [](int h, int c) { return h * DP + (c ^ (h << 3)); };
-            if (S::kCodes) {
+            auto at = [](int h, int c) { return h * DP + (c ^ ((h >> 1) << 3)); };
 #pragma unroll
-                for (int c = 0; c < S::kChunks; ++c)
-                    *reinterpret_cast<float4 *>(mine + at(g, 16 * c + 4 * t4)) =
-                        make_float4(o[2 * c][0] + o[2 * c][2], o[2 * c + 1][0] + o[2 * c + 1][2],
-                                    o[2 * c][1] + o[2 * c][3], o[2 * c + 1][1] + o[2 * c + 1][3]);
-            } else {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int c = 0; c < S::kTiles; ++c)
-                    *reinterpret_cast<float2 *>(mine + at(g, 8 * c + 2 * t4)) =
-                        make_float2(o[c][0] + o[c][2], o[c][1] + o[c][3]);
+                for (int x = 4; x < 32; x <<= 1)
+                    l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+                if (g == 0)
+                    sm_m[warp][2 * t4 + h] = m[h], sm_l[warp][2 * t4 + h] = l[h];
+#pragma unroll
+                for (int c = 0; c < S::kSteps; ++c) {
+                    if (S::kCodes) {
+                        *reinterpret_cast<float2 *>(mine + at(2 * t4 + h, 16 * c + 2 * g)) =
+                            make_float2(o[c][h], o[c][2 + h]);
+                    } else {
+                        mine[at(2 * t4 + h, 16 * c + g)] = o[c][h];
+                        mine[at(2 * t4 + h, 16 * c + g + 8)] = o[c][2 + h];
+                    }
+                }
             }
-            if (t4 == 0)
-                sm_m[warp][g] = m, sm_l[warp][g] = l;
             __syncthreads();
             const bool whole = unit_done && ubeg >= begin;
-            float *ws_ml = reinterpret_cast<float *>(a.ws + kMaxCtas * 4);
-            float *ws_o = ws_ml + kMaxCtas * 2 * 2 * kHeads;
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (ubeg >= begin ? 1 : 0);
-            for (int h = warp; h < heads; h += kWarps) {
-                float top = -INFINITY, sum_l = 0.f, f[kWarps];
+            uint32_t *ctr = reinterpret_cast<uint32_t *>(a.ws);
+            Pieces<DP> pc;
+            pc.ml = reinterpret_cast<float *>(ctr + 3 * kMaxCtas);
+            pc.o = pc.ml + kMaxCtas * 2 * 2 * kHeads;
+            const int64_t piece = 2 * (int64_t)blockIdx.x + (ubeg >= begin ? 1 : 0);
+            const float shift = BF ? 0.f : 14.f;
+            auto finish = [&](int h, int c, float4 x, float inv) {
+                *reinterpret_cast<float4 *>(a.out + use.r * a.ldo + (int64_t)(h0 + h) * D + c) =
+                    make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            };
+            auto finish_lse = [&](int h, float top, float sum_l) {
+                if (a.lse && lane == 0)
+                    a.lse[use.r * a.heads + h0 + h] = sum_l == 0.f ? -INFINITY : (top - shift) * kLn2 + logf(sum_l);
+            };
+            for (int h = warp; h < heads; h += W) {
+                float top = -INFINITY, sum_l = 0.f, f[W];
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
+                for (int w = 0; w < W; ++w)
                     top = fmaxf(top, sm_m[w][h]);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    f[w] = top == -INFINITY ? 0.f : ex2(sm_m[w][h] - top);
-                    sum_l = fmaf(sm_l[w][h], f[w], sum_l);
+                for (int w = 0; w < W; ++w) {
+                    f[w] = sm_m[w][h] == -INFINITY ? 0.f : ex2(sm_m[w][h] - top);
+                    sum_l += sm_l[w][h] != sm_l[w][h] ? sm_l[w][h] : sm_l[w][h] * f[w];
                 }
                 const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
                 for (int c = 4 * lane; c < D; c += 128) {
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
+                    for (int w = 0; w < W; ++w) {
                         const float4 y = *reinterpret_cast<const float4 *>(
                             smem + (w * S::kStages + stage) * S::kStage + at(h, c) * 4);
                         x.x = fmaf(y.x, f[w], x.x), x.y = fmaf(y.y, f[w], x.y);
                         x.z = fmaf(y.z, f[w], x.z), x.w = fmaf(y.w, f[w], x.w);
                     }
                     if (whole)
-                        *reinterpret_cast<float4 *>(a.out + use.r * a.ldo + (int64_t)(h0 + h) * D + c) =
-                            make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+                        finish(h, c, x, inv);
                     else
-                        *reinterpret_cast<float4 *>(ws_o + (slot * kHeads + h) * DP + c) = x;
+                        *reinterpret_cast<float4 *>(pc.at_o(piece, h) + c) = x;
                 }
-                if (lane == 0) {
-                    if (!whole) {
-                        ws_ml[(slot * kHeads + h) * 2] = top;
-                        ws_ml[(slot * kHeads + h) * 2 + 1] = sum_l;
-                    } else if (a.lse) {
-                        a.lse[use.r * a.heads + h0 + h] =
-                            sum_l == 0.f ? -INFINITY : (top - (BF ? 0.f : 14.f)) * kLn2 + logf(sum_l);
-                    }
-                }
+                if (whole)
+                    finish_lse(h, top, sum_l);
+                else if (lane == 0)
+                    *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
             }
             if (!whole) {
-                // the blocks that hold a piece: from the one with the unit's
-                // first tile to the one with its last
-                const int64_t c0 = ((ubeg + 1) * G + total - 1) / total - 1;
-                const int64_t c1 = (uend * G + total - 1) / total - 1;
-                uint32_t *ctr = reinterpret_cast<uint32_t *>(a.ws) + c0;
-                __threadfence();
-                __syncthreads();
-                if (tid == 0)
-                    last = atomicAdd(ctr, 1u) == (uint32_t)(c1 - c0);
-                __syncthreads();
-                if (last) {
+                // the blocks that hold a piece, from the one with the unit's
+                // first tile (its second piece) to the one with its last
+                // (their first pieces), sixteen to a bunch
+                const int c0 = (int)(((ubeg + 1) * G + total - 1) / total - 1);
+                const int c1 = (int)((uend * G + total - 1) / total - 1);
+                const int bunches = (c1 - c0) / kFan + 1, bunch = ((int)blockIdx.x - c0) / kFan;
+                const int b0 = c0 + bunch * kFan, count = min(kFan, c1 - b0 + 1);
+                auto piece_of = [&](int b) { return 2 * (int64_t)b + (b == c0 ? 1 : 0); };
+                auto arrive = [&](uint32_t *ctr, int of) {   // whether this block is the last of `of`
                     __threadfence();
-                    const int64_t first_slot = 2 * c0 + 1;   // the unit begins in block c0, ...
-                    for (int h = warp; h < heads; h += kWarps) {
-                        float top = -INFINITY, sum_l = 0.f;
-                        for (int64_t b = c0 + lane; b <= c1; b += 32) {
-                            const int64_t sl = b == c0 ? first_slot : 2 * b;   // ... and goes on in the others
-                            top = fmaxf(top, __ldcg(ws_ml + (sl * kHeads + h) * 2));
-                        }
-#pragma unroll
-                        for (int x = 16; x; x >>= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                        float4 x[DP / 128 ? DP / 128 : 1] = {};
-                        for (int64_t b = c0; b <= c1; ++b) {
-                            const int64_t sl = b == c0 ? first_slot : 2 * b;
-                            const float f = top == -INFINITY ? 0.f : ex2(__ldcg(ws_ml + (sl * kHeads + h) * 2) - top);
-                            sum_l = fmaf(__ldcg(ws_ml + (sl * kHeads + h) * 2 + 1), f, sum_l);
-#pragma unroll
-                            for (int q = 0; q < (DP / 128 ? DP / 128 : 1); ++q) {
-                                const int c = 4 * lane + 128 * q;
-                                if (c >= D)
-                                    continue;
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(ws_o + (sl * kHeads + h) * DP + c));
-                                x[q].x = fmaf(y.x, f, x[q].x), x[q].y = fmaf(y.y, f, x[q].y);
-                                x[q].z = fmaf(y.z, f, x[q].z), x[q].w = fmaf(y.w, f, x[q].w);
-                            }
-                        }
+                    __syncthreads();
+                    if (tid == 0) {
+                        const bool is = atomicAdd(ctr, 1u) == (uint32_t)of - 1;
+                        if (is)
+                            *ctr = 0;
+                        last = is;
+                    }
+                    __syncthreads();
+                    if (!last)
+                        return false;
+                    __threadfence();
+                    return true;
+                };
+                auto join_all = [&](int count, auto from, bool out) {
+                    for (int h = warp; h < heads; h += W) {
+                        float4 x[DP > 128 ? 2 : 1];
+                        float top, sum_l;
+                        join<DP>(pc, count, h, from, x, top, sum_l);
                         const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
 #pragma unroll
-                        for (int q = 0; q < (DP / 128 ? DP / 128 : 1); ++q) {
+                        for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
                             const int c = 4 * lane + 128 * q;
-                            if (c < D)
-                                *reinterpret_cast<float4 *>(a.out + use.r * a.ldo + (int64_t)(h0 + h) * D + c) =
-                                    make_float4(x[q].x * inv, x[q].y * inv, x[q].z * inv, x[q].w * inv);
+                            if (c >= D)
+                                continue;
+                            if (out)
+                                finish(h, c, x[q], inv);
+                            else
+                                *reinterpret_cast<float4 *>(pc.at_o(piece_of(b0), h) + c) = x[q];
                         }
-                        if (a.lse && lane == 0)
-                            a.lse[use.r * a.heads + h0 + h] =
-                                sum_l == 0.f ? -INFINITY : (top - (BF ? 0.f : 14.f)) * kLn2 + logf(sum_l);
+                        if (out)
+                            finish_lse(h, top, sum_l);
+                        else if (lane == 0)
+                            *reinterpret_cast<float2 *>(pc.at_ml(piece_of(b0), h)) = make_float2(top, sum_l);
                     }
-                    if (tid == 0)
-                        *ctr = 0;
+                };
+                if (arrive(ctr + piece_of(b0), count)) {
+                    join_all(count, [&](int i) { return piece_of(b0 + i); }, bunches == 1);
+                    if (bunches > 1 && arrive(ctr + 2 * kMaxCtas + c0, bunches))
+                        join_all(bunches, [&](int i) { return piece_of(c0 + i * kFan); }, true);
                 }
             }
             __syncthreads();   // the stages and sums are read
@@ -705,17 +793,16 @@ cudaError_t launch(const PagedAttention &a, uint32_t *err, cudaStream_t stream)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    // Two blocks an SM where the stages allow it; no more blocks than tiles
-    // that the block table can hold.
-    const int per_sm = 2 * (S::kSmem + 2048) <= 227 * 1024 ? 2 : 1;
+    // As many blocks as are resident; no more than tiles that the block table
+    // can hold.
     const int64_t group = a.heads / a.cache.kv_heads;
     const int64_t units = a.cache.kv_heads * ceil_div(group, kHeads);
     const int64_t span = a.max_pages * a.cache.page_size;
-    const int64_t tiles = a.requests * units * ceil_div(span < INT32_MAX ? span : INT32_MAX, kTile);
-    int64_t grid = (int64_t)sms * per_sm;
+    const int64_t tiles = a.requests * units * ceil_div(span < INT32_MAX ? span : INT32_MAX, S::kTile);
+    int64_t grid = (int64_t)sms * S::kBlocks;
     grid = grid < kMaxCtas ? grid : kMaxCtas;
     grid = grid < tiles ? grid : tiles;
-    k<<<(unsigned)grid, kThreads, S::kSmem, stream>>>(a, err);
+    k<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a, err);
     return cudaGetLastError();
 }
 
@@ -731,11 +818,11 @@ cudaError_t launch_type(const PagedAttention &a, uint32_t *err, cudaStream_t str
 
 }  // namespace
 
-// A counter per block, then maxima and sums, then sums of values of two
-// pieces per block (the first and the last of its run).
+// Counters (one per piece, one per block), then maxima and sums, then sums of
+// values of two pieces per block: the first and the last of its run.
 int64_t paged_attention_ws_bytes(int64_t head_dim)
 {
-    return kMaxCtas * 4 + (int64_t)kMaxCtas * 2 * kHeads * 4 * (2 + padded(head_dim));
+    return kMaxCtas * 3 * 4 + (int64_t)kMaxCtas * 2 * kHeads * 4 * (2 + padded(head_dim));
 }
 
 cudaError_t launch_paged_attention(const PagedAttention &a, uint32_t *err, cudaStream_t stream)
