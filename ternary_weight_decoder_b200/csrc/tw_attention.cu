@@ -22,7 +22,9 @@
 // an MMA, eight query heads its columns, so no lane computes for nobody:
 // scores^T = K q^T, out^T = V^T w^T.  The operands that are not in the cache
 // are carried in parts, each the rounding of what the last one left: two of
-// fp16 (22 bits), three of bf16 (24 bits), the scores and sums in fp32.
+// fp16 (22 bits), three of bf16 (24 bits); queries on codes in three int8
+// digits (23 bits of the head's largest), whose products are exact integers.
+// Scores and sums are fp32.
 // Groups of more than eight heads are split into units of eight.
 #include <cfloat>
 
@@ -30,6 +32,9 @@
 
 #ifndef TW_ATT_WARPS
 #define TW_ATT_WARPS 8
+#endif
+#ifndef TW_ATT_WARPS_CODES
+#define TW_ATT_WARPS_CODES 12
 #endif
 #ifndef TW_ATT_BLOCKS
 #define TW_ATT_BLOCKS 1
@@ -52,24 +57,27 @@ template <int DT, int DP>
 struct Shape {
     static constexpr bool kCodes = DT == TW_KV_I8;
     static constexpr bool kBf = DT == TW_KV_BF16;
-    static constexpr int kParts = kBf ? 3 : 2;         // of queries and weights
+    static constexpr int kParts = kBf ? 3 : 2;         // of a weight
     static constexpr int kElem = kCodes ? 1 : 2;
     static constexpr int kRow = DP * kElem;            // bytes of a key
     static constexpr int kChunks = kRow / 16;
     static constexpr int kPool = kKeys * kRow;         // bytes of a step's keys
-    static constexpr int kStage = 2 * kPool + (kCodes ? 2 * kKeys * 4 : 0);
-    static constexpr int kSteps = DP / 16;             // MMA steps over the columns
-    static constexpr int kWarps = DP > 128 ? TW_ATT_WARPS / 2 : TW_ATT_WARPS;
+    static constexpr int kStage = 2 * kPool;
+    static constexpr int kScales = kCodes ? 2 * kKeys * 4 : 0;   // of a stage, behind the rings
+    static constexpr int kSteps = DP / 16;             // 16 columns of values each
+    static constexpr int kQueryParts = kBf || kCodes ? 3 : 2;
+    static constexpr int kQuerySteps = kCodes ? DP / 32 : DP / 16;   // MMA steps over a key
+    static constexpr int kWarps = (kCodes ? TW_ATT_WARPS_CODES : TW_ATT_WARPS) / (DP > 128 ? 2 : 1);
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kKeys * kWarps;
     static constexpr int kBlocks = TW_ATT_BLOCKS;      // resident on an SM
     // Queries in registers up to 128 columns, in shared memory above.
     static constexpr bool kQueryShared = DP > 128 || TW_ATT_QS;
-    static constexpr int kQueryBytes = kQueryShared ? kSteps * 32 * 8 * kParts : 0;
-    static constexpr int kRoom = (227 * 1024) / kBlocks - 2048 - kQueryBytes;
-    static constexpr int kFit = kRoom / (kWarps * kStage);
+    static constexpr int kQueryBytes = kQueryShared ? kQuerySteps * 32 * 8 * kQueryParts : 0;
+    static constexpr int kRoom = (227 * 1024) / kBlocks - 3072 - kQueryBytes;
+    static constexpr int kFit = kRoom / (kWarps * (kStage + kScales));
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
-    static constexpr int kSmem = kWarps * kStages * kStage + kQueryBytes;
+    static constexpr int kSmem = kWarps * kStages * (kStage + kScales) + kQueryBytes;
     static_assert(kStages >= 2, "two stages at least");
     static_assert(kHeads * DP * 4 <= kStage, "a stage holds a warp's sums");
 };
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     using S = Shape<DT, DP>;
     constexpr bool BF = S::kBf;
     constexpr int W = S::kWarps, kThreads = S::kThreads, kTile = S::kTile;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t part[W];
     __shared__ int64_t start_r;
     __shared__ int start_u, start_t, last;
@@ -352,40 +360,52 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     // ---- the ring of stages
     constexpr int kRowsPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;   // rows of one pass of the warp
     const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
+    const uint32_t scales = smem_u32(smem) + W * S::kStages * S::kStage + warp * S::kStages * S::kScales;
     const int row0 = lane / S::kChunks, chunk = lane % S::kChunks;
-    const uint32_t lane_dst = place<S::kChunks>(row0, chunk);
+    const uint32_t lane_dst = ring + place<S::kChunks>(row0, chunk);
     const int64_t row_bytes = a.cache.token_stride * S::kElem;
     const uint8_t *kpool = static_cast<const uint8_t *>(a.cache.k) + row0 * row_bytes + chunk * 16;
-    const uint8_t *vpool = static_cast<const uint8_t *>(a.cache.v) + row0 * row_bytes + chunk * 16;
+    const int64_t v_of_k = static_cast<const uint8_t *>(a.cache.v) - static_cast<const uint8_t *>(a.cache.k);
+    const float *scale_pool = (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + (lane & 15) * kvh;
     const bool in_row = chunk < D * S::kElem / 16;
-    const bool page_steps = P % kKeys == 0;   // the 16 keys of a step share a page
+    // Steps whose 16 keys share a page, in pools with strides below 4 GB (one
+    // wide multiply-add each), take the short way.
+    const int64_t page_bytes = a.cache.page_stride * S::kElem, head_bytes = a.cache.head_stride * S::kElem;
+    const bool short_way = P % kKeys == 0 && ((page_bytes | head_bytes | row_bytes) >> 32) == 0;
     const int page_shift = (P & (P - 1)) == 0 ? __ffs(P) - 1 : -1;
     auto fetch = [&](int stage) {
         const int head = load.u / per_kv;
         const int j0 = (load.s.first_tile + load.t) * kTile + warp * kKeys;
-        const uint32_t base = ring + stage * S::kStage;
+        const uint32_t base = stage * S::kStage;
         const int32_t *table = a.block_table + load.r * a.table_stride;
-        if (page_steps && j0 >= load.s.lo && j0 + kKeys <= load.s.hi) {
+        if (short_way && j0 >= load.s.lo && j0 + kKeys <= load.s.hi) {
             const int p = page_shift >= 0 ? j0 >> page_shift : j0 / P;
             const int page = __ldg(table + p);
             if ((uint32_t)page < (uint32_t)a.cache.num_pages) {
                 const int in = j0 - p * P;
-                const int64_t off = (page * a.cache.page_stride + in * a.cache.token_stride +
-                                     head * a.cache.head_stride) * S::kElem;
-                const uint8_t *ks = kpool + off, *vs = vpool + off;
+                const uint8_t *ks = kpool + (uint64_t)(uint32_t)page * (uint32_t)page_bytes +
+                                    (uint64_t)(uint32_t)in * (uint32_t)row_bytes +
+                                    (uint64_t)(uint32_t)head * (uint32_t)head_bytes;
+                const uint8_t *vs = ks + v_of_k;
+                if (in_row) {
 #pragma unroll
-                for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                    const uint32_t dst = base + (lane_dst ^ (row_swap<S::kChunks>(kRowsPer * i) << 4)) +
-                                         kRowsPer * i * S::kRow;
-                    cp_async16(dst, in_row ? ks : kpool, in_row);
-                    cp_async16(dst + S::kPool, in_row ? vs : kpool, in_row);
-                    ks += kRowsPer * row_bytes, vs += kRowsPer * row_bytes;
+                    for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                        const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
+                        cp_async16(dst + kRowsPer * i * S::kRow, ks, true);
+                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, vs, true);
+                        ks += kRowsPer * row_bytes, vs += kRowsPer * row_bytes;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                        const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
+                        cp_async16(dst + kRowsPer * i * S::kRow, a.cache.k, false);
+                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, a.cache.k, false);
+                    }
                 }
-                if (S::kCodes) {
-                    const int64_t slot = ((int64_t)page * P + in + (lane & 15)) * kvh + head;
-                    cp_async4(base + 2 * S::kPool + lane * 4,
-                              (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + slot, true);
-                }
+                if (S::kCodes)
+                    cp_async4(scales + stage * S::kScales + lane * 4,
+                              scale_pool + (uint64_t)(uint32_t)(page * P + in) * (uint32_t)kvh + head, true);
                 if (lane == 0)
                     sm_mask[warp][stage] = 0xffffu;
                 return;
@@ -401,7 +421,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 const int in = j - p * P;
                 off = (page * a.cache.page_stride + in * a.cache.token_stride + head * a.cache.head_stride) *
                       S::kElem;
-                slot = ((int64_t)page * P + in) * kvh + head;
+                slot = ((int64_t)page * P + in - (lane & 15)) * kvh + head;
             } else {
                 ok = false;
                 atomicOr(err, EFLAG_BADDESC);
@@ -415,13 +435,12 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             const int row = row0 + kRowsPer * i;
             const int64_t o = __shfl_sync(0xffffffffu, off, row) - row0 * row_bytes;
             const bool in = ((mask >> row) & 1) && in_row;
-            const uint32_t dst = base + place<S::kChunks>(row, chunk);
+            const uint32_t dst = ring + base + place<S::kChunks>(row, chunk);
             cp_async16(dst, in ? kpool + o : a.cache.k, in);
-            cp_async16(dst + S::kPool, in ? vpool + o : a.cache.v, in);
+            cp_async16(dst + S::kPool, in ? kpool + v_of_k + o : a.cache.k, in);
         }
         if (S::kCodes)
-            cp_async4(base + 2 * S::kPool + lane * 4,
-                      (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + (ok ? slot : 0), ok);
+            cp_async4(scales + stage * S::kScales + lane * 4, ok ? scale_pool + slot : a.cache.k_scale, ok);
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
@@ -437,9 +456,9 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
 
     // Queries as the MMA's B operand, in parts: [step][part] the pairs of
     // columns (head g of the unit) that this lane feeds.
-    constexpr int kQ = S::kQueryShared ? 1 : S::kSteps;
-    uint32_t qb[kQ][S::kParts][2];
-    uint2 *qs = reinterpret_cast<uint2 *>(smem + W * S::kStages * S::kStage);
+    constexpr int kQ = S::kQueryShared ? 1 : S::kQuerySteps;
+    uint32_t qb[kQ][S::kQueryParts][2];
+    uint2 *qs = reinterpret_cast<uint2 *>(smem + W * S::kStages * (S::kStage + S::kScales));
     float o[S::kSteps][4];           // (columns g, g + 8 of 16) x (heads 2 t4, 2 t4 + 1)
     float m[2], l[2], unscale[2];    // of heads 2 t4, 2 t4 + 1
     int stage = 0;
@@ -452,52 +471,83 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             const bool live = (use.u % per_kv) * kHeads + g < group;
             const float *row = a.q + use.r * a.ldq + (int64_t)(h0 + (live ? g : 0)) * D;
             const float mul = a.scale * kLog2e;
-            // columns of step j that this lane holds.  Codes: four in a row,
-            // even and odd ones apart, as codes2 takes them out of a word.
-            auto load4 = [&](int j, float (&x)[4]) {
-                const int c0 = S::kCodes ? 16 * j + 4 * t4 : 16 * j + 2 * t4;
-                const int c1 = S::kCodes ? c0 + 2 : c0 + 8;
-                const float2 p = live && c0 < D ? *reinterpret_cast<const float2 *>(row + c0) : make_float2(0.f, 0.f);
-                const float2 q = live && c1 < D ? *reinterpret_cast<const float2 *>(row + c1) : make_float2(0.f, 0.f);
-                x[0] = p.x * mul, x[1] = (S::kCodes ? q.x : p.y) * mul;
-                x[2] = (S::kCodes ? p.y : q.x) * mul, x[3] = q.y * mul;
+            // a head's columns are spread over the four lanes of its quad:
+            // pairs of fp16 or bf16, or four bytes, as the MMA takes them
+            constexpr int kHold = S::kCodes ? 8 : 4;
+            auto hold = [&](int j, float (&x)[kHold]) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int c = S::kCodes ? 32 * j + 16 * k + 4 * t4 : 16 * j + 8 * k + 2 * t4;
+#pragma unroll
+                    for (int e = 0; e < kHold / 2; e += 2) {
+                        const float2 p = live && c + e < D ? *reinterpret_cast<const float2 *>(row + c + e)
+                                                           : make_float2(0.f, 0.f);
+                        x[k * (kHold / 2) + e] = p.x * mul, x[k * (kHold / 2) + e + 1] = p.y * mul;
+                    }
+                }
             };
             float norm = 1.f, back = 1.f;
             if (!BF) {
                 // fp16 operands: the head's largest query is brought to 2^14
-                // by a power of two, so that neither part leaves the range
-                float top = 0.f;
+                // by a power of two, so that no part leaves the range.  For
+                // codes it is brought below 2^23 - 2^15, the most that three
+                // balanced digits of eight bits hold, and rounded there.
+                float top = 0.f, poison = 0.f;   // poison: NaN if a query is, or is infinite
 #pragma unroll
-                for (int j = 0; j < S::kSteps; ++j) {
-                    float x[4];
-                    load4(j, x);
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+                for (int j = 0; j < S::kQuerySteps; ++j) {
+                    float x[kHold];
+                    hold(j, x);
+#pragma unroll
+                    for (int k = 0; k < kHold; ++k)
+                        top = fmaxf(top, fabsf(x[k])), poison = fmaf(x[k], 0.f, poison);
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+                poison += __shfl_xor_sync(0xffffffffu, poison, 1);
+                poison += __shfl_xor_sync(0xffffffffu, poison, 2);
                 const bool some = top > 0.f && top <= FLT_MAX;
-                norm = some ? __uint_as_float((uint32_t)(127 + 14 - e) << 23) : 1.f;
-                back = some ? __uint_as_float((uint32_t)(127 - 14 + e) << 23) : 1.f;
+                constexpr int kAt = S::kCodes ? 22 : 14;
+                const int e = min(max((int)(__float_as_uint(S::kCodes ? top * 1.0078125f : top) >> 23) - 127, -100), 127);
+                norm = some ? __uint_as_float((uint32_t)(127 + kAt - e) << 23) : 1.f;
+                back = (some ? __uint_as_float((uint32_t)(127 - kAt + e) << 23) : 1.f) + poison;
             }
             unscale[0] = __shfl_sync(0xffffffffu, back, 8 * t4);
             unscale[1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
 #pragma unroll
-            for (int j = 0; j < S::kSteps; ++j) {
+            for (int j = 0; j < S::kQuerySteps; ++j) {
                 if (S::kQueryShared && j % W != warp)
                     continue;
-                float x[4];
-                load4(j, x);
+                float x[kHold];
+                hold(j, x);
+                uint32_t b[S::kQueryParts][2];
+                if constexpr (S::kCodes) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x[k] *= norm;
+                    for (int k = 0; k < S::kQueryParts; ++k)
+                        b[k][0] = b[k][1] = 0;
 #pragma unroll
-                for (int k = 0; k < S::kParts; ++k) {
-                    const uint32_t b0 = split2<BF>(x[0], x[1]), b1 = split2<BF>(x[2], x[3]);
+                    for (int e = 0; e < kHold; ++e) {
+                        int v = __float2int_rn(x[e] * norm);   // = 2^16 d0 + 2^8 d1 + d2
+#pragma unroll
+                        for (int k = S::kQueryParts - 1; k >= 0; --k) {
+                            const int d = k ? ((v + 128) & 255) - 128 : v;
+                            b[k][e / 4] |= (uint32_t)(d & 255) << (8 * (e & 3));
+                            v = (v - d) >> 8;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k] *= norm;
+#pragma unroll
+                    for (int k = 0; k < S::kQueryParts; ++k)
+                        b[k][0] = split2<BF>(x[0], x[1]), b[k][1] = split2<BF>(x[2], x[3]);
+                }
+#pragma unroll
+                for (int k = 0; k < S::kQueryParts; ++k) {
                     if (S::kQueryShared)
-                        qs[(j * S::kParts + k) * 32 + lane] = make_uint2(b0, b1);
+                        qs[(j * S::kQueryParts + k) * 32 + lane] = make_uint2(b[k][0], b[k][1]);
                     else
-                        qb[S::kQueryShared ? 0 : j][k][0] = b0, qb[S::kQueryShared ? 0 : j][k][1] = b1;
+                        qb[S::kQueryShared ? 0 : j][k][0] = b[k][0], qb[S::kQueryShared ? 0 : j][k][1] = b[k][1];
                 }
             }
             if (S::kQueryShared)
@@ -517,64 +567,73 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         }
         commit();
 
-        const uint32_t kbase = ring + stage * S::kStage, vbase = kbase + S::kPool;
+        const uint32_t base = ring + stage * S::kStage;
         const uint32_t mask = sm_mask[warp][stage];
         if (mask) {
             // ---- scores of keys g, g + 8 for heads 2 t4, 2 t4 + 1
-            float acc[S::kParts][4] = {};
-            auto score = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            // (keys 0-7, 8-15) x (16 bytes at chunk 2 j, at 2 j + 1)
+            const uint32_t kbase = base + place<S::kChunks>(lane & 15, lane >> 4);
+            float sc[4];
+            if constexpr (S::kCodes) {
+                int acc[S::kQueryParts][4] = {};
 #pragma unroll
-                for (int k = 0; k < S::kParts; ++k) {
-                    uint32_t b0, b1;
-                    if (S::kQueryShared) {
-                        const uint2 v = qs[(j * S::kParts + k) * 32 + lane];
-                        b0 = v.x, b1 = v.y;
-                    } else {
-                        b0 = qb[S::kQueryShared ? 0 : j][k][0], b1 = qb[S::kQueryShared ? 0 : j][k][1];
-                    }
-                    mma<BF>(acc[k], a0, a1, a2, a3, b0, b1);
-                }
-            };
-            if (S::kCodes) {
-#pragma unroll
-                for (int j = 0; j < S::kSteps; j += 2) {
-                    uint32_t f[4];   // (keys 0-7, 8-15) x (chunks j, j + 1)
-                    ldmatrix4<false>(f, kbase + place<S::kChunks>(lane & 15, j + (lane >> 4)));
-                    score(j, codes2<false>(f[0]), codes2<false>(f[1]), codes2<true>(f[0]), codes2<true>(f[1]));
-                    score(j + 1, codes2<false>(f[2]), codes2<false>(f[3]), codes2<true>(f[2]), codes2<true>(f[3]));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < S::kSteps; ++j) {
+                for (int j = 0; j < S::kQuerySteps; ++j) {
                     uint32_t f[4];
-                    ldmatrix4<false>(f, kbase + place<S::kChunks>(lane & 15, 2 * j + (lane >> 4)));
-                    score(j, f[0], f[1], f[2], f[3]);
+                    ldmatrix4<false>(f, kbase ^ (j << 5));
+#pragma unroll
+                    for (int k = 0; k < S::kQueryParts; ++k) {
+                        const uint2 v = S::kQueryShared ? qs[(j * S::kQueryParts + k) * 32 + lane]
+                                                        : make_uint2(qb[S::kQueryShared ? 0 : j][k][0],
+                                                                     qb[S::kQueryShared ? 0 : j][k][1]);
+                        mma_s8_16832(acc[k], f[0], f[1], f[2], f[3], v.x, v.y);
+                    }
+                }
+                // exact sums of each digit (below 2^23); one rounding each below
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sc[e] = fmaf((float)(acc[0][e] * 256 + acc[1][e]), 256.f, (float)acc[2][e]);
+            } else {
+                float acc[S::kQueryParts][4] = {};
+#pragma unroll
+                for (int j = 0; j < S::kQuerySteps; ++j) {
+                    uint32_t f[4];
+                    ldmatrix4<false>(f, kbase ^ (j << 5));
+#pragma unroll
+                    for (int k = 0; k < S::kQueryParts; ++k) {
+                        const uint2 v = S::kQueryShared ? qs[(j * S::kQueryParts + k) * 32 + lane]
+                                                        : make_uint2(qb[S::kQueryShared ? 0 : j][k][0],
+                                                                     qb[S::kQueryShared ? 0 : j][k][1]);
+                        mma<BF>(acc[k], f[0], f[1], f[2], f[3], v.x, v.y);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sc[e] = acc[0][e] + acc[1][e];
+                    if (S::kQueryParts == 3)
+                        sc[e] += acc[S::kQueryParts - 1][e];
                 }
             }
             // ---- running maximum and sum.  With codes the value's scale goes
             // into the weight (as its logarithm, so that weights stay within
             // fp16 whatever the scales are): w_j = 2^(s_j + log2 vs_j - m).
-            float s[4], lv[2] = {0.f, 0.f}, ks[2] = {1.f, 1.f};
+            float s[4], lv[2] = {0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[e] = BF ? sc[e] : sc[e] * unscale[e & 1];
             if (S::kCodes) {
-                const float *sc = reinterpret_cast<const float *>(
-                    smem + (warp * S::kStages + stage) * S::kStage + 2 * S::kPool);
+                const float *of = reinterpret_cast<const float *>(
+                    smem + W * S::kStages * S::kStage + (warp * S::kStages + stage) * S::kScales);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    ks[k] = sc[g + 8 * k];
-                    const float vs = sc[kKeys + g + 8 * k];
+                    const float ks = of[g + 8 * k], vs = of[kKeys + g + 8 * k];
+                    s[2 * k] *= ks, s[2 * k + 1] *= ks;
                     lv[k] = vs > 0.f ? __log2f(vs) : 0.f;
                 }
             }
+            if (mask != 0xffffu) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = acc[0][e] + acc[1][e];
-                if (S::kParts == 3)
-                    x += acc[S::kParts - 1][e];
-                if (!BF)
-                    x *= unscale[e & 1];
-                if (S::kCodes)
-                    x *= ks[e >> 1];
-                s[e] = (mask >> (g + 8 * (e >> 1))) & 1 ? x : -INFINITY;
+                for (int e = 0; e < 4; ++e)
+                    s[e] = (mask >> (g + 8 * (e >> 1))) & 1 ? s[e] : -INFINITY;
             }
             float top[2];
 #pragma unroll
@@ -617,25 +676,31 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 w[k][1] = transpose8(split2<BF>(p[2], p[3]));
             }
             // ---- weighted values: columns x heads
+            if constexpr (S::kCodes) {
+                // byte pairs: keys 2 t4 + {0, 1}, columns 2 g + {0, 1} of chunks
+                // c, c + 1; even columns are the MMA's rows 0-7, odd ones 8-15
+                const uint32_t vbase = base + S::kPool + place<S::kChunks>(lane & 15, lane >> 4);
 #pragma unroll
-            for (int c = 0; c < S::kSteps; c += S::kCodes ? 2 : 1) {
-                uint32_t f[4];
-                if (S::kCodes) {
-                    // byte pairs: keys 2 t4 + {0, 1}, columns 2 g + {0, 1} of
-                    // chunks c, c + 1; even columns are rows 0-7, odd ones 8-15
-                    ldmatrix4<true>(f, vbase + place<S::kChunks>(lane & 15, c + (lane >> 4)));
+                for (int c = 0; c < S::kSteps; c += 2) {
+                    uint32_t f[4];
+                    ldmatrix4<true>(f, vbase ^ (c << 4));
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const uint32_t a0 = codes2<false>(f[2 * q]), a1 = codes2<true>(f[2 * q]);
                         const uint32_t a2 = codes2<false>(f[2 * q + 1]), a3 = codes2<true>(f[2 * q + 1]);
 #pragma unroll
                         for (int k = 0; k < S::kParts; ++k)
-                            mma<BF>(o[S::kCodes ? c + q : c], a0, a1, a2, a3, w[k][0], w[k][1]);
+                            mma<BF>(o[c + q], a0, a1, a2, a3, w[k][0], w[k][1]);
                     }
-                } else {
-                    // (columns 0-7, 8-15) x (keys 0-7, 8-15)
-                    ldmatrix4<true>(f, vbase + place<S::kChunks>((lane & 7) + ((lane >> 4) << 3),
-                                                                  2 * c + ((lane >> 3) & 1)));
+                }
+            } else {
+                // (columns 0-7, 8-15) x (keys 0-7, 8-15)
+                const uint32_t vbase = base + S::kPool +
+                                       place<S::kChunks>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+#pragma unroll
+                for (int c = 0; c < S::kSteps; ++c) {
+                    uint32_t f[4];
+                    ldmatrix4<true>(f, vbase ^ (c << 5));
 #pragma unroll
                     for (int k = 0; k < S::kParts; ++k)
                         mma<BF>(o[c], f[0], f[1], f[2], f[3], w[k][0], w[k][1]);
