@@ -594,7 +594,10 @@ TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads
  * outputs that it enters NaN or infinite.  A length past max_pages * page_size and
  * a page outside the pools record TW_ERR_CORRUPT: the keys concerned are left
  * out.  Sums and softmax statistics are fp32; the products' operands are
- * carried with at least 21 significant bits (cache elements exactly).
+ * carried with at least 21 significant bits (cache elements exactly), but
+ * queries to no less than 2^-23 of their head's largest and, on TW_KV_F16 and
+ * TW_KV_I8, weights (times their value's scale) to no less than 2^-37 of the
+ * largest.
  * TW_KV_I8: the scales of visible keys and values are 0 or in
  * [2^-60, 2^60].  heads: a multiple of kv_heads.
  */

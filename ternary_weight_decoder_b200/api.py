@@ -503,65 +503,98 @@ tw_decoder_chain_cached = _sig("tw_decoder_chain_cached", _int,
                                [_p, _p, _int, _p, _p, _p, _sz, _p])
 
 
-def _launch(call, device, stream, used):
-    """Run ``call(raw_stream)`` on ``device`` and raise on its status.  With a
-    stream other than the current one, the tensors in ``used`` are kept from
-    reuse until that stream has passed this point."""
-    index = device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(call, device, stream, used)
-    current = torch._C._cuda_getCurrentRawStream(index)
-    raw = current if stream is None else stream.cuda_stream
-    status = call(raw)
+# These calls stand between kernels of a few microseconds, so their checks read
+# each property of a tensor once and look for the words only to refuse it.
+_F32, _F64, _I32, _I8, _U8 = torch.float32, torch.float64, torch.int32, torch.int8, torch.uint8
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
+def _launch(fn, index, stream, used, *args):
+    """Call ``fn(*args, raw_stream)`` on device ``index`` and raise on its
+    status.  With a stream other than the current one, the tensors in ``used``
+    are kept from reuse until that stream has passed this point."""
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return _launch(fn, index, stream, used, *args)
+    if stream is None:
+        status = fn(*args, _raw_stream(index))
+        if status:
+            _raise(status)
+        return
+    status = fn(*args, stream.cuda_stream)
     if status:
         _raise(status)
-    if raw != current:
+    if stream.cuda_stream != _raw_stream(index):
         for t in used:
             if t is not None:
                 t.record_stream(stream)
 
 
-def _new(size, dtype, device, stream):
-    """An output made on the stream that writes it."""
+def _new(beside, size, dtype, stream):
+    """An output on the device of ``beside``, made on the stream that writes it."""
     if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
+        return beside.new_empty(size, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=dtype, device=device)
+        return beside.new_empty(size, dtype=dtype)
 
 
-def _want(t, dtype, shape, name, device):
-    """A contiguous tensor of this type, shape (None: any size) and device."""
+def _refuse(t, dtype, shape, name, index):
+    """Say what is wrong with a tensor that has not this type, shape (None:
+    any size), device or memory order."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a tensor of {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
     if len(t.shape) != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _want_rows(t, shape, name, device):
+def _device_of(t, name):
+    """Index of the CUDA device that a tensor is on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _vector(t, dtype, n, name, index):
+    """A contiguous tensor of n elements in one dimension."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or \
+            t.shape != (n,) or not t.is_contiguous():
+        _refuse(t, dtype, (n,), name, index)
+
+
+def _rows(t, rows, width, name, index):
     """An fp32 matrix whose rows are contiguous (any row stride); returns the stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
-        raise TypeError(f"{name} must be a tensor of torch.float32")
-    if len(t.shape) != 2 or any(w is not None and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
-    ld, last = t.stride()
-    if last != 1 and t.shape[1] > 1:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.get_device() != index or \
+            t.shape != (rows, width):
+        _refuse(t, _F32, (rows, width), name, index)
+    if rows <= 1:
+        if width > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return -(-width // 4) * 4   # one row has no stride of its own
+    ld, step = t.stride()
+    if step != 1 and width > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] <= 1:
-        return -(-t.shape[1] // 4) * 4   # one row has no stride of its own
     return ld
 
 
-def _cuda_device(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+def _table(t, requests, index):
+    """A block table [requests, max_pages] with contiguous rows; returns (max_pages, row stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 2 or \
+            t.shape[0] != requests or t.get_device() != index:
+        _refuse(t, _I32, (requests, None), "block_table", index)
+    pages = t.shape[1]
+    if pages > 1 and t.stride(1) != 1:
+        raise ValueError("block_table must have contiguous rows")
+    return pages, t.stride(0) if requests > 1 else pages
+
+
+def _matrix(t, name):
+    """The shape of a two-dimensional tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, has {t.dim()}")
+    return t.shape
 
 
 def _data(t):
@@ -577,10 +610,12 @@ class KVCache:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
-        self.device = _cuda_device(k, "k")
+        self.index = _device_of(k, "k")
+        self.device = k.device
         if k.dtype not in KV_DTYPES:
             raise TypeError(f"pools must be one of {list(KV_DTYPES)}, got {k.dtype}")
-        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        if not isinstance(v, torch.Tensor) or k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or \
+                v.device != k.device:
             raise ValueError("k and v must be alike: [num_pages, page_size, kv_heads, head_dim]")
         # A dimension of size 1 has no stride of its own.
         strides = [s if n > 1 else 0 for n, s in zip(k.shape, k.stride())]
@@ -591,14 +626,17 @@ class KVCache:
         if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
             raise ValueError("int8 pools come with k_scale and v_scale, others without")
         if k_scale is not None:
-            _want(k_scale, torch.float32, k.shape[:3], "k_scale", self.device)
-            _want(v_scale, torch.float32, k.shape[:3], "v_scale", self.device)
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.shape != k.shape[:3] or \
+                        t.get_device() != self.index or not t.is_contiguous():
+                    _refuse(t, _F32, k.shape[:3], name, self.index)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         strides = [s or -(-self.head_dim // 16) * 16 for s in strides]
         self.struct = KVCacheStruct(_data(k), _data(v), _data(k_scale), _data(v_scale), *k.shape,
                                     *strides[:3], KV_DTYPES[k.dtype])
         self.ref = ctypes.addressof(self.struct)
+        self.scale = self.head_dim ** -0.5
         self.tensors = (k, v, k_scale, v_scale)
 
     @classmethod
@@ -633,40 +671,34 @@ def kv_assign(lengths: torch.Tensor, delta: torch.Tensor, block_table: torch.Ten
     stride) and ``free_pages`` are updated in place, and each new token gets a
     row.  ``lengths_out`` and ``free_count_out`` may be the inputs themselves.
     A step that does not fit changes nothing and is reported by ``check``."""
-    device = _cuda_device(lengths, "lengths")
-    i32 = torch.int32
-    _want(lengths, i32, (None,), "lengths", device)
-    n = lengths.shape[0]
-    _want(delta, i32, (n,), "delta", device)
-    _want(free_pages, i32, (None,), "free_pages", device)
-    _want(free_count, i32, (1,), "free_count", device)
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != i32:
-        raise TypeError(f"block_table must be a tensor of {i32}")
-    if block_table.dim() != 2 or block_table.shape[0] != n or block_table.device != device or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [requests, max_pages] with contiguous rows, beside lengths")
-    width = block_table.shape[1]
-    stride = block_table.stride(0) if n > 1 else width
+    index = _device_of(lengths, "lengths")
+    n = lengths.shape[0] if lengths.dim() else None
+    _vector(lengths, _I32, n, "lengths", index)
+    _vector(delta, _I32, n, "delta", index)
+    capacity = len(free_pages) if isinstance(free_pages, torch.Tensor) and free_pages.dim() else None
+    _vector(free_pages, _I32, capacity, "free_pages", index)
+    _vector(free_count, _I32, 1, "free_count", index)
+    width, stride = _table(block_table, n, index)
     if rows < 0:
         raise ValueError("rows must be >= 0")
     if lengths_out is None:
-        lengths_out = _new(n, i32, device, stream)
+        lengths_out = _new(lengths, (n,), _I32, stream)
     else:
-        _want(lengths_out, i32, (n,), "lengths_out", device)
+        _vector(lengths_out, _I32, n, "lengths_out", index)
     if free_count_out is None:
-        free_count_out = _new(1, i32, device, stream)
+        free_count_out = _new(lengths, (1,), _I32, stream)
     else:
-        _want(free_count_out, i32, (1,), "free_count_out", device)
-    per_row = _new((3, rows), i32, device, stream)
+        _vector(free_count_out, _I32, 1, "free_count_out", index)
+    per_row = _new(lengths, (3, rows), _I32, stream)
     slots, positions, requests = per_row.unbind(0)
-    row_start = _new(n + 1, i32, device, stream)
+    row_start = _new(lengths, (n + 1,), _I32, stream)
     at = per_row.data_ptr()
-    _launch(lambda s: tw_kv_assign(
-        lengths.data_ptr(), delta.data_ptr(), n, page_size, block_table.data_ptr(), width, stride,
-        free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), lengths_out.data_ptr(),
-        free_count_out.data_ptr(), at, at + 4 * rows, at + 8 * rows, rows, row_start.data_ptr(), s),
-        device, stream, (lengths, delta, block_table, free_pages, free_count, lengths_out,
-                         free_count_out, per_row, row_start))
+    _launch(tw_kv_assign, index, stream,
+            (lengths, delta, block_table, free_pages, free_count, lengths_out, free_count_out, per_row,
+             row_start),
+            lengths.data_ptr(), delta.data_ptr(), n, page_size, block_table.data_ptr(), width, stride,
+            free_pages.data_ptr(), capacity, free_count.data_ptr(), lengths_out.data_ptr(),
+            free_count_out.data_ptr(), at, at + 4 * rows, at + 8 * rows, rows, row_start.data_ptr())
     return KVAssignment(lengths_out, free_count_out, slots, positions, requests, row_start)
 
 
@@ -677,30 +709,32 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     positions [rows] * inv_freq [rotary / 2] (fp64; None: no rotation), write
     k and v into the cache at slots [rows] (negative: not written) and return
     the rotated queries (``q_out``; may be q).  Rows may be strided."""
-    device = _cuda_device(q, "q")
-    wide = cache.kv_heads * cache.head_dim
-    ldq = _want_rows(q, (None, None), "q", device)
-    rows, width = q.shape
-    if width % cache.head_dim:
-        raise ValueError(f"q has {width} columns, not whole heads of {cache.head_dim}")
-    ldk = _want_rows(k, (rows, wide), "k", device)
-    ldv = _want_rows(v, (rows, wide), "v", device)
-    _want(positions, torch.int32, (rows,), "positions", device)
-    _want(slots, torch.int32, (rows,), "slots", device)
-    if cache.device != device:
-        raise ValueError(f"the cache must be on {device}, is on {cache.device}")
-    rotary = 0
-    if inv_freq is not None:
-        _want(inv_freq, torch.float64, (None,), "inv_freq", device)
-        rotary = 2 * inv_freq.shape[0]
+    index = _device_of(q, "q")
+    rows, width = _matrix(q, "q")
+    dim = cache.head_dim
+    wide = cache.kv_heads * dim
+    heads = width // dim
+    if heads * dim != width:
+        raise ValueError(f"q has {width} columns, not whole heads of {dim}")
+    ldq = _rows(q, rows, width, "q", index)
+    ldk = _rows(k, rows, wide, "k", index)
+    ldv = _rows(v, rows, wide, "v", index)
+    _vector(positions, _I32, rows, "positions", index)
+    _vector(slots, _I32, rows, "slots", index)
+    if cache.index != index:
+        raise ValueError(f"the cache must be on cuda:{index}, is on {cache.device}")
+    rotary = freq = None
+    if inv_freq is not None and len(inv_freq):
+        rotary, freq = 2 * len(inv_freq), inv_freq.data_ptr()
+        _vector(inv_freq, _F64, rotary // 2, "inv_freq", index)
     if q_out is None:
-        q_out = _new((rows, width), torch.float32, device, stream)
-    ldqo = _want_rows(q_out, (rows, width), "q_out", device)
-    _launch(lambda s: tw_rope_append(
-        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, width // cache.head_dim, rotary,
-        inv_freq.data_ptr() if rotary else None, interleaved, positions.data_ptr(), slots.data_ptr(),
-        cache.ref, q_out.data_ptr(), ldqo, s),
-        device, stream, (q, k, v, positions, slots, inv_freq, q_out) + cache.tensors)
+        q_out = _new(q, (rows, width), _F32, stream)
+        ldqo = width
+    else:
+        ldqo = _rows(q_out, rows, width, "q_out", index)
+    _launch(tw_rope_append, index, stream, (q, k, v, positions, slots, inv_freq, q_out) + cache.tensors,
+            q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, heads, rotary or 0, freq,
+            interleaved, positions.data_ptr(), slots.data_ptr(), cache.ref, q_out.data_ptr(), ldqo)
     return q_out
 
 
@@ -722,46 +756,43 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     [requests, max_pages]; scale is 1 / sqrt(head_dim) by default.  Returns out,
     or (out, lse) with the log-sum-exps [requests, heads].  ``ws`` comes from
     ``paged_attention_workspace`` (None: one is made for the call)."""
-    device = _cuda_device(q, "q")
-    ldq = _want_rows(q, (None, None), "q", device)
-    n, width = q.shape
-    if width % cache.head_dim:
-        raise ValueError(f"q has {width} columns, not whole heads of {cache.head_dim}")
+    index = _device_of(q, "q")
+    n, width = _matrix(q, "q")
     heads = width // cache.head_dim
-    if cache.device != device:
-        raise ValueError(f"the cache must be on {device}, is on {cache.device}")
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
-        raise TypeError("block_table must be a tensor of torch.int32")
-    if block_table.dim() != 2 or block_table.shape[0] != n or block_table.device != device or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [requests, max_pages] with contiguous rows, beside q")
-    pages = block_table.shape[1]
-    stride = block_table.stride(0) if n > 1 else pages
-    _want(lengths, torch.int32, (n,), "lengths", device)
+    if heads * cache.head_dim != width:
+        raise ValueError(f"q has {width} columns, not whole heads of {cache.head_dim}")
+    if cache.index != index:
+        raise ValueError(f"the cache must be on cuda:{index}, is on {cache.device}")
+    ldq = _rows(q, n, width, "q", index)
+    pages, stride = _table(block_table, n, index)
+    _vector(lengths, _I32, n, "lengths", index)
     if first is not None:
-        _want(first, torch.int32, (n,), "first", device)
+        _vector(first, _I32, n, "first", index)
     if out is None:
-        out = _new((n, width), torch.float32, device, stream)
-    ldo = _want_rows(out, (n, width), "out", device)
+        out = _new(q, (n, width), _F32, stream)
+        ldo = width
+    else:
+        ldo = _rows(out, n, width, "out", index)
     if lse is not None:
-        _want(lse, torch.float32, (n, heads), "lse", device)
+        if not isinstance(lse, torch.Tensor) or lse.dtype is not _F32 or lse.get_device() != index or \
+                lse.shape != (n, heads) or not lse.is_contiguous():
+            _refuse(lse, _F32, (n, heads), "lse", index)
     elif return_lse:
-        lse = _new((n, heads), torch.float32, device, stream)
+        lse = _new(q, (n, heads), _F32, stream)
     if ws is None:
         if stream is None:
             ws = paged_attention_workspace(n, heads, cache)
         else:
             with torch.cuda.stream(stream):
                 ws = paged_attention_workspace(n, heads, cache)
-    else:
-        _want(ws, torch.uint8, (None,), "ws", device)
+    size = len(ws)
+    _vector(ws, _U8, size, "ws", index)
     if scale is None:
-        scale = cache.head_dim ** -0.5
-    _launch(lambda s: tw_paged_attention(
-        q.data_ptr(), ldq, n, heads, cache.ref, block_table.data_ptr(), pages, stride,
-        lengths.data_ptr(), _data(first), scale, out.data_ptr(), ldo, _data(lse), ws.data_ptr(),
-        ws.shape[0], s),
-        device, stream, (q, block_table, lengths, first, out, lse, ws) + cache.tensors)
+        scale = cache.scale
+    _launch(tw_paged_attention, index, stream,
+            (q, block_table, lengths, first, out, lse, ws) + cache.tensors,
+            q.data_ptr(), ldq, n, heads, cache.ref, block_table.data_ptr(), pages, stride,
+            lengths.data_ptr(), _data(first), scale, out.data_ptr(), ldo, _data(lse), ws.data_ptr(), size)
     return (out, lse) if return_lse else out
 
 
@@ -790,48 +821,56 @@ def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str |
     ``quantize`` gives the int8 codes of n (as ``quantize_act``) in its
     place, ready for ``ternary_linear_q``.  h and n may be passed in, h may be
     x and n may be y."""
-    device = _cuda_device(x, "x")
-    ldx = _want_rows(x, (None, None), "x", device)
-    size = x.shape
-    rows, width = size
+    index = _device_of(x, "x")
+    rows, width = _matrix(x, "x")
+    size = (rows, width)
+    ldx = _rows(x, rows, width, "x", index)
     if post not in NORMS or pre not in NORMS:
         raise ValueError(f"post and pre must be one of {list(NORMS)}")
-    ldy = 0 if y is None else _want_rows(y, size, "y", device)
+    ldy = 0 if y is None else _rows(y, rows, width, "y", index)
     ldg = 0
     if gate is not None:
         if gate.dim() == 1:
-            _want(gate, torch.float32, (width,), "gate", device)
+            _vector(gate, _F32, width, "gate", index)
         else:
-            ldg = _want_rows(gate, size, "gate", device)
-    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
-                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        if t is not None:
-            _want(t, torch.float32, (width,), name, device)
-    if quantize and n is not None:
-        raise ValueError("quantize gives codes: n cannot be passed in")
+            ldg = _rows(gate, rows, width, "gate", index)
+    if post_weight is not None:
+        _vector(post_weight, _F32, width, "post_weight", index)
+    if post_bias is not None:
+        _vector(post_bias, _F32, width, "post_bias", index)
+    if pre_weight is not None:
+        _vector(pre_weight, _F32, width, "pre_weight", index)
+    if pre_bias is not None:
+        _vector(pre_bias, _F32, width, "pre_bias", index)
     ldh = ldn = 0
-    if y is None and h is None:
-        out_h = None   # h is x as it stands
-    else:
-        out_h = _new(size, torch.float32, device, stream) if h is None else h
-        ldh = _want_rows(out_h, size, "h", device)
+    if h is not None:
+        ldh = _rows(h, rows, width, "h", index)
+    elif y is not None:
+        h = _new(x, size, _F32, stream)
+        ldh = width
+    # (neither: h is x as it stands)
     xq = amax = qsum = None
     if quantize:
-        xq = _new(size, torch.int8, device, stream)
-        amax = _new(rows, torch.float32, device, stream)
-        qsum = _new(rows, torch.int32, device, stream)
-    elif pre is not None or n is not None:
-        n = _new(size, torch.float32, device, stream) if n is None else n
-        ldn = _want_rows(n, size, "n", device)
-    elif out_h is None:
+        if n is not None:
+            raise ValueError("quantize gives codes: n cannot be passed in")
+        xq = _new(x, size, _I8, stream)
+        amax = _new(x, (rows,), _F32, stream)
+        qsum = _new(x, (rows,), _I32, stream)
+    elif n is not None:
+        ldn = _rows(n, rows, width, "n", index)
+    elif pre is not None:
+        n = _new(x, size, _F32, stream)
+        ldn = width
+    elif h is None:
         raise ValueError("nothing to compute: no y, no norm and no codes")
     args = NormArgs(x.data_ptr(), _data(y), _data(gate), _data(post_weight), _data(post_bias),
-                    _data(pre_weight), _data(pre_bias), _data(out_h), _data(n), _data(xq),
-                    _data(amax), _data(qsum), rows, width, ldx, ldy, ldg, ldh, ldn, NORMS[post],
-                    NORMS[pre], alpha, eps)
-    _launch(lambda s: tw_residual_norm(ctypes.byref(args), s), device, stream,
-            (x, y, gate, post_weight, post_bias, pre_weight, pre_bias, out_h, n, xq, amax, qsum))
-    return NormResult(x if out_h is None else out_h, n, xq, amax, qsum)
+                    _data(pre_weight), _data(pre_bias), _data(h), _data(n), _data(xq), _data(amax),
+                    _data(qsum), rows, width, ldx, ldy, ldg, ldh, ldn, NORMS[post], NORMS[pre], alpha,
+                    eps)
+    _launch(tw_residual_norm, index, stream,
+            (x, y, gate, post_weight, post_bias, pre_weight, pre_bias, h, n, xq, amax, qsum),
+            ctypes.byref(args))
+    return NormResult(x if h is None else h, n, xq, amax, qsum)
 
 
 # ------------------------------------- decoder-layer chain with its cache
@@ -851,19 +890,17 @@ class CachedDecoderChain(DecoderChain):
         super().__init__(layers, M, hidden, kv_dim, head_dim, inter, device, acc_out=acc_out)
         if len(caches) != len(layers) or len(norms) != len(layers):
             raise ValueError("one cache and one pair of norm gains per layer")
-        dev = self.h.device
+        dev, index = self.h.device, self.h.get_device()
         for t, name in ((lengths, "lengths"), (positions, "positions"), (slots, "slots"), (first, "first")):
             if t is not None or name != "first":
-                _want(t, torch.int32, (M,), name, dev)
-        _want(block_table, torch.int32, (M, None), "block_table", dev)
+                _vector(t, _I32, M, name, index)
+        pages, stride = _table(block_table, M, index)
         if inv_freq is not None:
-            _want(inv_freq, torch.float64, (None,), "inv_freq", dev)
-        _want(norm_out, torch.float32, (hidden,), "norm_out", dev)
-        for pair in norms:
-            for t in pair:
-                _want(t, torch.float32, (hidden,), "norm gain", dev)
+            _vector(inv_freq, _F64, len(inv_freq), "inv_freq", index)
+        for t in [norm_out] + [t for pair in norms for t in pair]:
+            _vector(t, _F32, hidden, "norm gain", index)
         for c in caches:
-            if c.device != dev:
+            if c.index != index:
                 raise ValueError(f"the caches must be on {dev}")
         self.x = torch.zeros((M, hidden), dtype=torch.float32, device=dev)
         self.caches, self.norms, self.norm_out = list(caches), list(norms), norm_out
@@ -876,7 +913,7 @@ class CachedDecoderChain(DecoderChain):
         self.c_cache = ChainCache(
             _data(self.x), _data(self.q), _data(self.k), _data(norm_out), _data(positions),
             _data(slots), _data(block_table), _data(lengths), _data(first), _data(inv_freq),
-            block_table.shape[1], block_table.shape[1],
+            pages, stride,
             0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved),
             head_dim ** -0.5 if scale is None else scale, eps, _data(self.attention_ws),
             self.attention_ws.numel())
@@ -884,7 +921,6 @@ class CachedDecoderChain(DecoderChain):
 
 def decoder_chain_cached(chain: CachedDecoderChain, stream=None):
     """Run every layer of ``chain`` for one new token per request."""
-    _launch(lambda s: tw_decoder_chain_cached(
-        chain.c_layers, chain.c_cached, chain.n_layers, ctypes.byref(chain.c_buf),
-        ctypes.byref(chain.c_cache), chain.ws.data_ptr(), chain.ws_bytes, s),
-        chain.h.device, stream, ())
+    _launch(tw_decoder_chain_cached, chain.h.get_device(), stream, (),
+            chain.c_layers, chain.c_cached, chain.n_layers, ctypes.byref(chain.c_buf),
+            ctypes.byref(chain.c_cache), chain.ws.data_ptr(), chain.ws_bytes)

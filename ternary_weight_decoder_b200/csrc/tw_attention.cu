@@ -14,7 +14,7 @@
 // to end, and every block takes an equal run of them, whatever the lengths
 // are.  A block whose run holds all of a (request, KV head) writes its
 // output; the pieces of one that spans blocks go to the workspace and are
-// joined in a fixed order, by the last block of every sixteen and then by the
+// joined in a fixed order, by the last block of every kFan and then by the
 // last of those.  Inside a block each warp takes 16 keys of every tile
 // through its own ring of cp.async stages: no barrier until a piece ends.
 //
@@ -36,11 +36,14 @@
 #ifndef TW_ATT_WARPS_CODES
 #define TW_ATT_WARPS_CODES 12
 #endif
+#ifndef TW_ATT_RUN
+#define TW_ATT_RUN 2
+#endif
+#ifndef TW_ATT_WHOLE
+#define TW_ATT_WHOLE 4
+#endif
 #ifndef TW_ATT_BLOCKS
 #define TW_ATT_BLOCKS 1
-#endif
-#ifndef TW_ATT_QS
-#define TW_ATT_QS 0
 #endif
 
 namespace tw {
@@ -49,8 +52,30 @@ namespace {
 constexpr int kKeys = 16;                    // keys of a warp's step
 constexpr int kMaxCtas = 512;                // counters and partial results in the workspace
 constexpr int kHeads = 8;                    // query heads of a unit
-constexpr int kFan = 16;                     // pieces that one block joins
+constexpr int kBatch = 16;                   // of them at a time
+constexpr int kFan = 96;                     // pieces that one block joins
+constexpr int kMinTile = 32;                 // keys of the smallest variant's tile
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+// A call, as the kernel reads it.
+struct Args {
+    const float *q;
+    float *out, *lse;
+    const int32_t *table, *lengths, *first;
+    const uint8_t *k;
+    int64_t v_of_k;                  // bytes from the keys to the values
+    const float *k_scale, *v_scale;
+    uint8_t *ws;
+    uint32_t *err;
+    int64_t ldq, ldo, table_stride;
+    int64_t page_bytes, row_bytes, head_bytes;
+    int requests, heads, kv_heads, group;
+    int per_kv, units;               // units of eight heads per KV head, and in all
+    int D, P, page_shift;            // page_shift: log2 P, or -1
+    int cap, pages;                  // keys that a table row can name, pages of the pools
+    int short_way;                   // 16 keys share a page, byte strides below 2^32
+    float mul;                       // scale * log2 e
+};
 
 // The shape of one variant: DP columns (head_dim rounded up) of type DT.
 template <int DT, int DP>
@@ -71,10 +96,8 @@ struct Shape {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kKeys * kWarps;
     static constexpr int kBlocks = TW_ATT_BLOCKS;      // resident on an SM
-    // Queries in registers up to 128 columns, in shared memory above.
-    static constexpr bool kQueryShared = DP > 128 || TW_ATT_QS;
-    static constexpr int kQueryBytes = kQueryShared ? kQuerySteps * 32 * 8 * kQueryParts : 0;
-    static constexpr int kRoom = (227 * 1024) / kBlocks - 3072 - kQueryBytes;
+    static constexpr int kQueryBytes = kQuerySteps * kQueryParts * 32 * 8;   // a unit's queries, as operands
+    static constexpr int kRoom = (227 * 1024) / kBlocks - 5120 - kQueryBytes;
     static constexpr int kFit = kRoom / (kWarps * (kStage + kScales));
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kWarps * kStages * (kStage + kScales) + kQueryBytes;
@@ -190,17 +213,10 @@ struct Span {
 };
 
 template <int TILE>
-__device__ __forceinline__ Span span_of(const PagedAttention &a, int64_t r, bool report, uint32_t *err)
+__device__ __forceinline__ Span span_of(const Args &a, int r)
 {
     Span s;
-    const int64_t cap = a.max_pages * a.cache.page_size;
-    int64_t hi = a.lengths[r];
-    if (hi > cap) {
-        hi = cap;
-        if (report)
-            atomicOr(err, EFLAG_BADDESC);
-    }
-    s.hi = (int)hi;
+    s.hi = min(a.lengths[r], a.cap);
     s.lo = a.first ? max(a.first[r], 0) : 0;
     s.first_tile = s.lo / TILE;
     s.tiles = s.hi > s.lo ? (s.hi - 1) / TILE + 1 - s.first_tile : 0;
@@ -210,36 +226,23 @@ __device__ __forceinline__ Span span_of(const PagedAttention &a, int64_t r, bool
 // A place in the run of tiles: tile t of unit u of request r.
 template <int TILE>
 struct Cursor {
-    int64_t r;
-    int u, t;
+    int r, u, t;
     Span s;
-    __device__ __forceinline__ void next(const PagedAttention &a, int units)
+    __device__ __forceinline__ void next(const Args &a)
     {
         if (++t < s.tiles)
             return;
         t = 0;
-        if (++u < units)
+        if (++u < a.units)
             return;
         u = 0;
         do {
-            ++r;
-            if (r >= a.requests)
+            if (++r >= a.requests)
                 return;
-            s = span_of<TILE>(a, r, false, nullptr);
+            s = span_of<TILE>(a, r);
         } while (s.tiles == 0);
     }
 };
-
-__device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane)
-{
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o)
-            v += u;
-    }
-    return v;
-}
 
 // The pieces of one unit in the workspace: maxima and sums [piece][head][2],
 // sums of values [piece][head][DP].
@@ -250,111 +253,129 @@ struct Pieces {
     __device__ __forceinline__ float *at_o(int64_t piece, int h) const { return o + (piece * kHeads + h) * DP; }
 };
 
-// Join `count` <= 32 pieces of head h, piece i being piece_of(i), by one
-// warp, in the order of i.  Columns 4 * lane + 128 q of the sum stay in x.
-template <int DP, class F>
-__device__ __forceinline__ void join(const Pieces<DP> &w, int count, int h, F piece_of,
-                                     float4 (&x)[DP > 128 ? 2 : 1], float &top, float &sum)
-{
-    const int lane = threadIdx.x & 31;
-    float m = -INFINITY, l = 0.f;
-    if (lane < count) {
-        const float2 v = __ldcg(reinterpret_cast<const float2 *>(w.at_ml(piece_of(lane), h)));
-        m = v.x, l = v.y;
+// How `total` tiles fall to G blocks: the first `more` take one more than `each`.
+struct Split {
+    uint32_t each, more;
+    __device__ __forceinline__ Split(uint32_t total, uint32_t G) : each(total / G), more(total - each * G) {}
+    __device__ __forceinline__ uint32_t begin(uint32_t block) const { return block * each + min(block, more); }
+    __device__ __forceinline__ int block_of(uint32_t tile) const
+    {
+        const uint32_t cut = more * (each + 1);
+        const bool low = tile < cut;
+        const uint32_t q = (low ? tile : tile - cut) / (low ? each + 1 : each);
+        return (int)(low ? q : more + q);
     }
-    top = m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = m == -INFINITY ? 0.f : ex2(m - top);
-    sum = l * f;   // (a piece without a maximum can hold a NaN sum: it stays one)
-    if (l != l)
-        sum = l;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-    for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
-        x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int c = min(4 * lane + 128 * q, DP - 4);
-#pragma unroll 8
-        for (int i = 0; i < count; ++i) {
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(w.at_o(piece_of(i), h) + c));
-            const float g = __shfl_sync(0xffffffffu, f, i);
-            x[q].x = fmaf(y.x, g, x[q].x), x[q].y = fmaf(y.y, g, x[q].y);
-            x[q].z = fmaf(y.z, g, x[q].z), x[q].w = fmaf(y.w, g, x[q].w);
-        }
-    }
-}
+};
 
 template <int DT, int DP>
 __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlocks)
-    k_paged_attention(const PagedAttention a, uint32_t *err)
+    k_paged_attention(const Args a)
 {
     using S = Shape<DT, DP>;
     constexpr bool BF = S::kBf;
     constexpr int W = S::kWarps, kThreads = S::kThreads, kTile = S::kTile;
+    // The running maximum is raised once a score passes it by this much (in
+    // powers of two), so that most steps leave the sums alone.  Weights are
+    // then up to 2^slack; fp16 ones are carried times 2^12 (as is the sum),
+    // so that the second part of small ones stays clear of fp16's smallest
+    // number and large ones below its largest.
+    constexpr float kSlack = BF ? 8.f : 3.f, kUp = BF ? 0.f : 12.f;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t part[W];
-    __shared__ int64_t start_r;
-    __shared__ int start_u, start_t, last;
-    __shared__ float sm_m[W][kHeads], sm_l[W][kHeads];
+    __shared__ uint32_t part[W];
+    __shared__ int start[3], last;
+    __shared__ uint32_t bounds[2];
+    __shared__ float sm_m[W][kHeads], sm_l[W][kHeads], sm_back[kHeads];
     __shared__ uint32_t sm_mask[W][S::kStages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int D = (int)a.cache.head_dim, P = (int)a.cache.page_size, kvh = (int)a.cache.kv_heads;
-    const int group = a.heads / kvh, per_kv = (group + kHeads - 1) / kHeads, units = kvh * per_kv;
-    const int64_t R = a.requests;
+    const int D = a.D;
+
+    // rows without keys
+    auto clear_rows = [&] {
+        for (int r = blockIdx.x; r < a.requests; r += gridDim.x) {
+            if (span_of<kTile>(a, r).tiles)
+                continue;
+            for (int c = tid; c < a.heads * D; c += kThreads)
+                a.out[r * a.ldo + c] = 0.f;
+            if (a.lse)
+                for (int h = tid; h < a.heads; h += kThreads)
+                    a.lse[(int64_t)r * a.heads + h] = -INFINITY;
+        }
+    };
 
     // ---- this block's run of tiles: lengths are scanned by every block
-    const int64_t per = (R + kThreads - 1) / kThreads;
-    const int64_t rlo = min((int64_t)tid * per, R), rhi = min(rlo + per, R);
-    int64_t sum = 0;
-    for (int64_t r = rlo; r < rhi; ++r)
-        sum += span_of<kTile>(a, r, blockIdx.x == 0, err).tiles;
-    const int64_t incl = warp_inclusive(sum, lane);
+    const int per = (a.requests + kThreads - 1) / kThreads;
+    const int rlo = min(tid * per, a.requests), rhi = min(rlo + per, a.requests);
+    uint32_t sum = 0;
+#pragma unroll 1
+    for (int r = rlo; r < rhi; ++r) {
+        sum += span_of<kTile>(a, r).tiles;
+        if (blockIdx.x == 0 && a.lengths[r] > a.cap)
+            atomicOr(a.err, EFLAG_BADDESC);
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += u;
+    }
     if (lane == 31)
         part[warp] = incl;
     __syncthreads();
-    int64_t before = incl - sum, total = 0;
+    uint32_t before = incl - sum, total = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         before += w < warp ? part[w] : 0;
         total += part[w];
     }
-    total *= units;
-    const int64_t G = min((int64_t)gridDim.x, total);   // blocks with tiles: no run between two is empty
-    const int64_t begin = blockIdx.x < G ? total * blockIdx.x / G : 0;
-    const int64_t end = blockIdx.x < G ? total * (blockIdx.x + 1) / G : 0;
-    if (begin < end && before * units <= begin && begin < (before + sum) * units) {
-        int64_t at = before * units, r = rlo;
-        for (;; ++r) {
-            const int64_t n = (int64_t)span_of<kTile>(a, r, false, nullptr).tiles * units;
-            if (begin < at + n) {
-                const int64_t tiles = n / units;
-                start_r = r;
-                start_u = (int)((begin - at) / tiles);
-                start_t = (int)((begin - at) % tiles);
-                break;
+    total *= a.units;
+    const uint32_t G = min(gridDim.x, (total + TW_ATT_RUN - 1) / TW_ATT_RUN);   // blocks with tiles
+    const Split split(total, max(G, 1u));
+    uint32_t begin = split.begin(min(blockIdx.x, G)), end = split.begin(min(blockIdx.x + 1, G));
+    if (begin < end) {
+        // Small units are not cut: a run's end inside one moves to the unit's
+        // nearer end, for this block and its neighbour alike.
+        const uint32_t small = max((uint32_t)TW_ATT_WHOLE, split.each / 4);
+        const uint32_t mine = before * a.units, past = (before + sum) * a.units;
+        if (tid == 0 && end == total)
+            bounds[1] = end;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t at = k ? end : begin;
+            if (at < mine || at >= past)
+                continue;
+            uint32_t in = at - mine;
+            Cursor<kTile> c;
+            for (c.r = rlo;; ++c.r) {
+                c.s = span_of<kTile>(a, c.r);
+                if (in < c.s.tiles * a.units)
+                    break;
+                in -= c.s.tiles * a.units;
             }
-            at += n;
+            c.u = in / c.s.tiles, c.t = in % c.s.tiles;
+            uint32_t to = at;
+            if (c.s.tiles <= small && c.t) {
+                const bool down = 2 * c.t < c.s.tiles;
+                to = down ? at - c.t : at + c.s.tiles - c.t;
+                c.t = down ? 0 : c.s.tiles - 1;
+                if (!down)
+                    c.next(a);
+            }
+            bounds[k] = to;
+            if (k == 0)
+                start[0] = c.r, start[1] = c.u, start[2] = c.t;
         }
     }
-    // rows without keys
-    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-        if (span_of<kTile>(a, r, false, nullptr).tiles)
-            continue;
-        for (int c = tid; c < a.heads * D; c += kThreads)
-            a.out[r * a.ldo + c] = 0.f;
-        if (a.lse)
-            for (int h = tid; h < a.heads; h += kThreads)
-                a.lse[r * a.heads + h] = -INFINITY;
-    }
     __syncthreads();
-    if (begin >= end)
+    if (begin < end)
+        begin = bounds[0], end = bounds[1];
+    if (begin >= end) {
+        clear_rows();
         return;
+    }
     Cursor<kTile> load, use;
-    load.r = start_r, load.u = start_u, load.t = start_t;
-    load.s = span_of<kTile>(a, load.r, false, nullptr);
+    load.r = start[0], load.u = start[1], load.t = start[2];
+    load.s = span_of<kTile>(a, load.r);
     use = load;
 
     // ---- the ring of stages
@@ -363,195 +384,193 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     const uint32_t scales = smem_u32(smem) + W * S::kStages * S::kStage + warp * S::kStages * S::kScales;
     const int row0 = lane / S::kChunks, chunk = lane % S::kChunks;
     const uint32_t lane_dst = ring + place<S::kChunks>(row0, chunk);
-    const int64_t row_bytes = a.cache.token_stride * S::kElem;
-    const uint8_t *kpool = static_cast<const uint8_t *>(a.cache.k) + row0 * row_bytes + chunk * 16;
-    const int64_t v_of_k = static_cast<const uint8_t *>(a.cache.v) - static_cast<const uint8_t *>(a.cache.k);
-    const float *scale_pool = (lane < 16 ? a.cache.k_scale : a.cache.v_scale) + (lane & 15) * kvh;
+    const uint8_t *kpool = a.k + row0 * a.row_bytes + chunk * 16;
+    const float *scale_pool = (lane < 16 ? a.k_scale : a.v_scale) + (lane & 15) * a.kv_heads;
     const bool in_row = chunk < D * S::kElem / 16;
-    // Steps whose 16 keys share a page, in pools with strides below 4 GB (one
-    // wide multiply-add each), take the short way.
-    const int64_t page_bytes = a.cache.page_stride * S::kElem, head_bytes = a.cache.head_stride * S::kElem;
-    const bool short_way = P % kKeys == 0 && ((page_bytes | head_bytes | row_bytes) >> 32) == 0;
-    const int page_shift = (P & (P - 1)) == 0 ? __ffs(P) - 1 : -1;
-    auto fetch = [&](int stage) {
-        const int head = load.u / per_kv;
-        const int j0 = (load.s.first_tile + load.t) * kTile + warp * kKeys;
-        const uint32_t base = stage * S::kStage;
-        const int32_t *table = a.block_table + load.r * a.table_stride;
-        if (short_way && j0 >= load.s.lo && j0 + kKeys <= load.s.hi) {
-            const int p = page_shift >= 0 ? j0 >> page_shift : j0 / P;
-            const int page = __ldg(table + p);
-            if ((uint32_t)page < (uint32_t)a.cache.num_pages) {
-                const int in = j0 - p * P;
-                const uint8_t *ks = kpool + (uint64_t)(uint32_t)page * (uint32_t)page_bytes +
-                                    (uint64_t)(uint32_t)in * (uint32_t)row_bytes +
-                                    (uint64_t)(uint32_t)head * (uint32_t)head_bytes;
-                const uint8_t *vs = ks + v_of_k;
-                if (in_row) {
-#pragma unroll
-                    for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                        const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
-                        cp_async16(dst + kRowsPer * i * S::kRow, ks, true);
-                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, vs, true);
-                        ks += kRowsPer * row_bytes, vs += kRowsPer * row_bytes;
-                    }
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                        const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
-                        cp_async16(dst + kRowsPer * i * S::kRow, a.cache.k, false);
-                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, a.cache.k, false);
-                    }
-                }
-                if (S::kCodes)
-                    cp_async4(scales + stage * S::kScales + lane * 4,
-                              scale_pool + (uint64_t)(uint32_t)(page * P + in) * (uint32_t)kvh + head, true);
-                if (lane == 0)
-                    sm_mask[warp][stage] = 0xffffu;
-                return;
-            }
+    // The next step's first key and, if its keys are visible and share a page
+    // (the short way), that page: looked up a step early.
+    int next_j = 0, next_in = 0, next_page = -1;
+    auto look_up = [&] {
+        next_j = (load.s.first_tile + load.t) * kTile + warp * kKeys;
+        next_page = -1;
+        if (a.short_way && next_j >= load.s.lo && next_j + kKeys <= load.s.hi) {
+            const int p = a.page_shift >= 0 ? next_j >> a.page_shift : next_j / a.P;
+            next_in = next_j - p * a.P;
+            next_page = __ldg(a.table + load.r * a.table_stride + p);
         }
-        const int j = j0 + (lane & 15);
+    };
+    uint32_t partial = 0;   // stages filled the long way: their masks are in sm_mask
+    auto fetch = [&](int stage) {
+        const int head = load.u / a.per_kv;
+        const uint32_t base = stage * S::kStage;
+        if ((uint32_t)next_page < (uint32_t)a.pages) {
+            const uint8_t *ks = kpool + (uint64_t)(uint32_t)next_page * (uint32_t)a.page_bytes +
+                                (uint64_t)(uint32_t)next_in * (uint32_t)a.row_bytes +
+                                (uint64_t)(uint32_t)head * (uint32_t)a.head_bytes;
+            const uint8_t *vs = ks + a.v_of_k;
+            if (DP * S::kElem >= 512 || in_row) {
+#pragma unroll
+                for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                    const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
+                    cp_async16(dst + kRowsPer * i * S::kRow, DP * S::kElem < 512 || in_row ? ks : a.k,
+                               DP * S::kElem < 512 || in_row);
+                    cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, DP * S::kElem < 512 || in_row ? vs : a.k,
+                               DP * S::kElem < 512 || in_row);
+                    ks += kRowsPer * a.row_bytes, vs += kRowsPer * a.row_bytes;
+                }
+            } else {   // past head_dim: zeros
+#pragma unroll 1
+                for (int i = 0; i < kKeys / kRowsPer; ++i) {
+                    const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
+                    cp_async16(dst + kRowsPer * i * S::kRow, a.k, false);
+                    cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, a.k, false);
+                }
+            }
+            if (S::kCodes)
+                cp_async4(scales + stage * S::kScales + lane * 4,
+                          scale_pool + (uint64_t)(uint32_t)(next_page * a.P + next_in) * (uint32_t)a.kv_heads + head,
+                          true);
+            partial &= ~(1u << stage);
+            return;
+        }
+        const int j = next_j + (lane & 15);
         bool ok = j >= load.s.lo && j < load.s.hi;
         int64_t off = 0, slot = 0;
         if (ok) {
-            const int p = j / P;
-            const int page = __ldg(table + p);
-            if ((uint32_t)page < (uint32_t)a.cache.num_pages) {
-                const int in = j - p * P;
-                off = (page * a.cache.page_stride + in * a.cache.token_stride + head * a.cache.head_stride) *
-                      S::kElem;
-                slot = ((int64_t)page * P + in - (lane & 15)) * kvh + head;
+            const int p = j / a.P;
+            const int page = __ldg(a.table + load.r * a.table_stride + p);
+            if ((uint32_t)page < (uint32_t)a.pages) {
+                const int in = j - p * a.P;
+                off = page * a.page_bytes + in * a.row_bytes + head * a.head_bytes;
+                slot = ((int64_t)page * a.P + in - (lane & 15)) * a.kv_heads + head;
             } else {
                 ok = false;
-                atomicOr(err, EFLAG_BADDESC);
+                atomicOr(a.err, EFLAG_BADDESC);
             }
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
         if (lane == 0)
             sm_mask[warp][stage] = mask;
+        partial |= 1u << stage;
 #pragma unroll 1
         for (int i = 0; i < kKeys / kRowsPer; ++i) {
             const int row = row0 + kRowsPer * i;
-            const int64_t o = __shfl_sync(0xffffffffu, off, row) - row0 * row_bytes;
+            const int64_t o = __shfl_sync(0xffffffffu, off, row) - row0 * a.row_bytes;
             const bool in = ((mask >> row) & 1) && in_row;
             const uint32_t dst = ring + base + place<S::kChunks>(row, chunk);
-            cp_async16(dst, in ? kpool + o : a.cache.k, in);
-            cp_async16(dst + S::kPool, in ? kpool + v_of_k + o : a.cache.k, in);
+            cp_async16(dst, in ? kpool + o : a.k, in);
+            cp_async16(dst + S::kPool, in ? kpool + a.v_of_k + o : a.k, in);
         }
         if (S::kCodes)
-            cp_async4(scales + stage * S::kScales + lane * 4, ok ? scale_pool + slot : a.cache.k_scale, ok);
+            cp_async4(scales + stage * S::kScales + lane * 4, ok ? scale_pool + slot : a.k_scale, ok);
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-    const int n = (int)(end - begin);
-#pragma unroll 1
-    for (int s = 0; s < S::kStages - 1; ++s) {
-        if (s < n) {
-            fetch(s);
-            load.next(a, units);
-        }
-        commit();
-    }
-
-    // Queries as the MMA's B operand, in parts: [step][part] the pairs of
-    // columns (head g of the unit) that this lane feeds.
-    constexpr int kQ = S::kQueryShared ? 1 : S::kQuerySteps;
-    uint32_t qb[kQ][S::kQueryParts][2];
+    // Queries as the MMA's B operand, in parts: [step][part][lane] the two
+    // words that a lane feeds for head lane / 4 of the unit.
     uint2 *qs = reinterpret_cast<uint2 *>(smem + W * S::kStages * (S::kStage + S::kScales));
     float o[S::kSteps][4];           // (columns g, g + 8 of 16) x (heads 2 t4, 2 t4 + 1)
     float m[2], l[2], unscale[2];    // of heads 2 t4, 2 t4 + 1
+    const int n = (int)(end - begin);
     int stage = 0;
     bool fresh = true;
+    look_up();
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        // ---- a new piece: its queries, split
+    for (int i = 1 - S::kStages; i < n; ++i) {
+        // ---- a stage ahead
+        if (i >= 0) {
+            cp_async_wait<S::kStages - 2>();
+            __syncwarp();   // every lane's copies of this stage are here, the last stage is read
+        }
+        if (i + S::kStages - 1 < n) {
+            fetch(i < 0 ? i + S::kStages - 1 : stage == 0 ? S::kStages - 1 : stage - 1);
+            load.next(a);
+            if (i + S::kStages < n)
+                look_up();
+        }
+        commit();
+        if (i < 0)
+            continue;
+
+        // ---- a new piece: its queries, a head to a warp, split
         if (fresh) {
-            const int h0 = (use.u / per_kv) * group + (use.u % per_kv) * kHeads;
-            const bool live = (use.u % per_kv) * kHeads + g < group;
-            const float *row = a.q + use.r * a.ldq + (int64_t)(h0 + (live ? g : 0)) * D;
-            const float mul = a.scale * kLog2e;
-            // a head's columns are spread over the four lanes of its quad:
-            // pairs of fp16 or bf16, or four bytes, as the MMA takes them
-            constexpr int kHold = S::kCodes ? 8 : 4;
-            auto hold = [&](int j, float (&x)[kHold]) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int c = S::kCodes ? 32 * j + 16 * k + 4 * t4 : 16 * j + 8 * k + 2 * t4;
-#pragma unroll
-                    for (int e = 0; e < kHold / 2; e += 2) {
-                        const float2 p = live && c + e < D ? *reinterpret_cast<const float2 *>(row + c + e)
-                                                           : make_float2(0.f, 0.f);
-                        x[k * (kHold / 2) + e] = p.x * mul, x[k * (kHold / 2) + e + 1] = p.y * mul;
-                    }
-                }
-            };
-            float norm = 1.f, back = 1.f;
-            if (!BF) {
-                // fp16 operands: the head's largest query is brought to 2^14
-                // by a power of two, so that no part leaves the range.  For
-                // codes it is brought below 2^23 - 2^15, the most that three
-                // balanced digits of eight bits hold, and rounded there.
+            const int h0 = (use.u / a.per_kv) * a.group + (use.u % a.per_kv) * kHeads;
+            const int heads = min(kHeads, a.group - (use.u % a.per_kv) * kHeads);
+#pragma unroll 1
+            for (int h = warp; h < kHeads; h += W) {
+                const float *row = a.q + use.r * a.ldq + (int64_t)(h0 + h) * D;
+                constexpr int kQuads = DP > 128 ? 2 : 1;
+                float x[kQuads][4];
                 float top = 0.f, poison = 0.f;   // poison: NaN if a query is, or is infinite
 #pragma unroll
-                for (int j = 0; j < S::kQuerySteps; ++j) {
-                    float x[kHold];
-                    hold(j, x);
-#pragma unroll
-                    for (int k = 0; k < kHold; ++k)
-                        top = fmaxf(top, fabsf(x[k])), poison = fmaf(x[k], 0.f, poison);
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                poison += __shfl_xor_sync(0xffffffffu, poison, 1);
-                poison += __shfl_xor_sync(0xffffffffu, poison, 2);
-                const bool some = top > 0.f && top <= FLT_MAX;
-                constexpr int kAt = S::kCodes ? 22 : 14;
-                const int e = min(max((int)(__float_as_uint(S::kCodes ? top * 1.0078125f : top) >> 23) - 127, -100), 127);
-                norm = some ? __uint_as_float((uint32_t)(127 + kAt - e) << 23) : 1.f;
-                back = (some ? __uint_as_float((uint32_t)(127 - kAt + e) << 23) : 1.f) + poison;
-            }
-            unscale[0] = __shfl_sync(0xffffffffu, back, 8 * t4);
-            unscale[1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
-#pragma unroll
-            for (int j = 0; j < S::kQuerySteps; ++j) {
-                if (S::kQueryShared && j % W != warp)
-                    continue;
-                float x[kHold];
-                hold(j, x);
-                uint32_t b[S::kQueryParts][2];
-                if constexpr (S::kCodes) {
-#pragma unroll
-                    for (int k = 0; k < S::kQueryParts; ++k)
-                        b[k][0] = b[k][1] = 0;
-#pragma unroll
-                    for (int e = 0; e < kHold; ++e) {
-                        int v = __float2int_rn(x[e] * norm);   // = 2^16 d0 + 2^8 d1 + d2
-#pragma unroll
-                        for (int k = S::kQueryParts - 1; k >= 0; --k) {
-                            const int d = k ? ((v + 128) & 255) - 128 : v;
-                            b[k][e / 4] |= (uint32_t)(d & 255) << (8 * (e & 3));
-                            v = (v - d) >> 8;
-                        }
-                    }
-                } else {
+                for (int q = 0; q < kQuads; ++q) {
+                    const int c = 4 * lane + 128 * q;
+                    const float4 v = h < heads && c < D ? *reinterpret_cast<const float4 *>(row + c)
+                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[q][0] = v.x * a.mul, x[q][1] = v.y * a.mul, x[q][2] = v.z * a.mul, x[q][3] = v.w * a.mul;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[k] *= norm;
-#pragma unroll
-                    for (int k = 0; k < S::kQueryParts; ++k)
-                        b[k][0] = split2<BF>(x[0], x[1]), b[k][1] = split2<BF>(x[2], x[3]);
+                        top = fmaxf(top, fabsf(x[q][k])), poison = fmaf(x[q][k], 0.f, poison);
                 }
+                float norm = 1.f, back = 1.f;
+                if (!BF) {
+                    // fp16 operands: the head's largest query is brought to 2^14
+                    // by a power of two, so that no part leaves the range.  For
+                    // codes it is brought below 2^23 - 2^15, the most that three
+                    // balanced digits of eight bits hold, and rounded there.
 #pragma unroll
-                for (int k = 0; k < S::kQueryParts; ++k) {
-                    if (S::kQueryShared)
-                        qs[(j * S::kQueryParts + k) * 32 + lane] = make_uint2(b[k][0], b[k][1]);
-                    else
-                        qb[S::kQueryShared ? 0 : j][k][0] = b[k][0], qb[S::kQueryShared ? 0 : j][k][1] = b[k][1];
+                    for (int s = 16; s; s >>= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                        poison += __shfl_xor_sync(0xffffffffu, poison, s);
+                    }
+                    const bool some = top > 0.f && top <= FLT_MAX;
+                    constexpr int kAt = S::kCodes ? 22 : 14;
+                    const int e = min(max((int)(__float_as_uint(S::kCodes ? top * 1.0078125f : top) >> 23) - 127, -100), 127);
+                    norm = some ? __uint_as_float((uint32_t)(127 + kAt - e) << 23) : 1.f;
+                    back = (some ? __uint_as_float((uint32_t)(127 - kAt + e) << 23) : 1.f) + poison;
+                }
+                if (lane == 0)
+                    sm_back[h] = back;
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q) {
+                    const int c = 4 * lane + 128 * q;   // columns c .. c + 3
+                    if (c >= DP)
+                        continue;
+                    if constexpr (S::kCodes) {
+                        uint32_t word[3] = {0, 0, 0};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            int v = __float2int_rn(x[q][e] * norm);   // = 2^16 d0 + 2^8 d1 + d2
+#pragma unroll
+                            for (int k = 2; k >= 0; --k) {
+                                const int d = k ? ((v + 128) & 255) - 128 : v;
+                                word[k] |= (uint32_t)(d & 255) << (8 * e);
+                                v = (v - d) >> 8;
+                            }
+                        }
+                        // step c / 32, half (c / 16) % 2, lane 4 h + (c / 4) % 4
+                        uint32_t *to = reinterpret_cast<uint32_t *>(qs + (c / 32) * 3 * 32 + 4 * h + (c / 4) % 4) +
+                                       (c / 16) % 2;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            to[k * 64] = word[k];
+                    } else {
+                        // step c / 16, half (c / 8) % 2, lanes 4 h + (c / 2) % 4 + {0, 1}
+                        uint32_t *to = reinterpret_cast<uint32_t *>(qs + (c / 16) * S::kQueryParts * 32 + 4 * h +
+                                                                    (c / 2) % 4) + (c / 8) % 2;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[q][e] *= norm;
+#pragma unroll
+                        for (int k = 0; k < S::kQueryParts; ++k) {
+                            to[k * 64] = split2<BF>(x[q][0], x[q][1]);
+                            to[k * 64 + 2] = split2<BF>(x[q][2], x[q][3]);
+                        }
+                    }
                 }
             }
-            if (S::kQueryShared)
-                __syncthreads();
+            __syncthreads();
+            unscale[0] = sm_back[2 * t4], unscale[1] = sm_back[2 * t4 + 1];
             m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
 #pragma unroll
             for (int c = 0; c < S::kSteps; ++c)
@@ -559,16 +578,8 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             fresh = false;
         }
 
-        cp_async_wait<S::kStages - 2>();
-        __syncwarp();   // every lane's copies of this stage are here, the last stage is read
-        if (i + S::kStages - 1 < n) {
-            fetch(stage == 0 ? S::kStages - 1 : stage - 1);
-            load.next(a, units);
-        }
-        commit();
-
         const uint32_t base = ring + stage * S::kStage;
-        const uint32_t mask = sm_mask[warp][stage];
+        const uint32_t mask = (partial >> stage) & 1 ? sm_mask[warp][stage] : 0xffffu;
         if (mask) {
             // ---- scores of keys g, g + 8 for heads 2 t4, 2 t4 + 1
             // (keys 0-7, 8-15) x (16 bytes at chunk 2 j, at 2 j + 1)
@@ -582,9 +593,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     ldmatrix4<false>(f, kbase ^ (j << 5));
 #pragma unroll
                     for (int k = 0; k < S::kQueryParts; ++k) {
-                        const uint2 v = S::kQueryShared ? qs[(j * S::kQueryParts + k) * 32 + lane]
-                                                        : make_uint2(qb[S::kQueryShared ? 0 : j][k][0],
-                                                                     qb[S::kQueryShared ? 0 : j][k][1]);
+                        const uint2 v = qs[(j * S::kQueryParts + k) * 32 + lane];
                         mma_s8_16832(acc[k], f[0], f[1], f[2], f[3], v.x, v.y);
                     }
                 }
@@ -600,9 +609,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     ldmatrix4<false>(f, kbase ^ (j << 5));
 #pragma unroll
                     for (int k = 0; k < S::kQueryParts; ++k) {
-                        const uint2 v = S::kQueryShared ? qs[(j * S::kQueryParts + k) * 32 + lane]
-                                                        : make_uint2(qb[S::kQueryShared ? 0 : j][k][0],
-                                                                     qb[S::kQueryShared ? 0 : j][k][1]);
+                        const uint2 v = qs[(j * S::kQueryParts + k) * 32 + lane];
                         mma<BF>(acc[k], f[0], f[1], f[2], f[3], v.x, v.y);
                     }
                 }
@@ -614,9 +621,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 }
             }
             // ---- running maximum and sum.  With codes the value's scale goes
-            // into the weight (as its logarithm, so that weights stay within
-            // fp16 whatever the scales are): w_j = 2^(s_j + log2 vs_j - m).
-            float s[4], lv[2] = {0.f, 0.f};
+            // into the weight, 2^(s_j - m) vs_j, and into the maximum, that of
+            // s_j + log2 vs_j, so that weights stay within fp16 whatever the
+            // scales are (the sum of 2^(s_j - m) need not: it is fp32).
+            float s[4], vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 s[e] = BF ? sc[e] : sc[e] * unscale[e & 1];
@@ -625,9 +633,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     smem + W * S::kStages * S::kStage + (warp * S::kStages + stage) * S::kScales);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float ks = of[g + 8 * k], vs = of[kKeys + g + 8 * k];
+                    const float ks = of[g + 8 * k];
+                    vs[k] = of[kKeys + g + 8 * k];
                     s[2 * k] *= ks, s[2 * k + 1] *= ks;
-                    lv[k] = vs > 0.f ? __log2f(vs) : 0.f;
+                    lv[k] = vs[k] > 0.f ? __log2f(vs[k]) : 0.f;
                 }
             }
             if (mask != 0xffffu) {
@@ -644,7 +653,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
-            if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+            if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
                 float f[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -659,15 +668,14 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     for (int e = 0; e < 4; ++e)
                         o[c][e] *= f[e & 1];
             }
-            // fp16 weights are carried times 2^14 (as is the sum), so that
-            // the second part of small ones stays clear of fp16's smallest
+            const float shift[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - kUp, (m[1] == -INFINITY ? 0.f : m[1]) - kUp};
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float shift = (m[e & 1] == -INFINITY ? 0.f : m[e & 1]) - (BF ? 0.f : 14.f);
-                const float x = s[e] - shift;
-                p[e] = ex2(S::kCodes ? x + lv[e >> 1] : x);
-                l[e & 1] += S::kCodes ? ex2(x) : p[e];
+                p[e] = ex2(s[e] - shift[e & 1]);
+                l[e & 1] += p[e];
+                if (S::kCodes)
+                    p[e] *= vs[e >> 1];
             }
             uint32_t w[S::kParts][2];
 #pragma unroll
@@ -711,9 +719,9 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         // ---- the end of a piece
         const bool unit_done = use.t + 1 == use.s.tiles;
         if (unit_done || i + 1 == n) {
-            const int64_t ubeg = begin + i - use.t, uend = ubeg + use.s.tiles;
-            const int h0 = (use.u / per_kv) * group + (use.u % per_kv) * kHeads;
-            const int heads = min(kHeads, group - (use.u % per_kv) * kHeads);
+            const uint32_t ubeg = begin + i - use.t, uend = ubeg + use.s.tiles;
+            const int h0 = (use.u / a.per_kv) * a.group + (use.u % a.per_kv) * kHeads;
+            const int heads = min(kHeads, a.group - (use.u % a.per_kv) * kHeads);
             __syncwarp();   // the stage is read: it takes the warp's sums
             float *mine = reinterpret_cast<float *>(smem + (warp * S::kStages + stage) * S::kStage);
             // [head][column], columns permuted by the head against bank conflicts
@@ -736,121 +744,168 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     }
                 }
             }
-            __syncthreads();
-            const bool whole = unit_done && ubeg >= begin;
             uint32_t *ctr = reinterpret_cast<uint32_t *>(a.ws);
             Pieces<DP> pc;
             pc.ml = reinterpret_cast<float *>(ctr + 3 * kMaxCtas);
             pc.o = pc.ml + kMaxCtas * 2 * 2 * kHeads;
-            const int64_t piece = 2 * (int64_t)blockIdx.x + (ubeg >= begin ? 1 : 0);
-            const float shift = BF ? 0.f : 14.f;
-            auto finish = [&](int h, int c, float4 x, float inv) {
-                *reinterpret_cast<float4 *>(a.out + use.r * a.ldo + (int64_t)(h0 + h) * D + c) =
-                    make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            const bool whole = unit_done && ubeg >= begin;
+            int64_t piece = 2 * (int64_t)blockIdx.x + (ubeg >= begin ? 1 : 0);
+            // ---- the warps' maxima, sums and sums of values, merged: a head to a warp
+            auto put = [&](bool out, int h, int c, float4 x, float inv) {
+                float *to = out ? a.out + use.r * a.ldo + (int64_t)(h0 + h) * D : pc.at_o(piece, h);
+                *reinterpret_cast<float4 *>(to + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
             };
-            auto finish_lse = [&](int h, float top, float sum_l) {
-                if (a.lse && lane == 0)
-                    a.lse[use.r * a.heads + h0 + h] = sum_l == 0.f ? -INFINITY : (top - shift) * kLn2 + logf(sum_l);
+            auto put_sum = [&](bool out, int h, float top, float sum_l) {
+                if (!out)
+                    *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
+                else if (a.lse)
+                    a.lse[(int64_t)use.r * a.heads + h0 + h] =
+                        sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
             };
+            __syncthreads();
+#pragma unroll 1
             for (int h = warp; h < heads; h += W) {
-                float top = -INFINITY, sum_l = 0.f, f[W];
+                // lane w has warp w's
+                const float wm = lane < W ? sm_m[lane % W][h] : -INFINITY, wl = lane < W ? sm_l[lane % W][h] : 0.f;
+                float top = wm;
 #pragma unroll
-                for (int w = 0; w < W; ++w)
-                    top = fmaxf(top, sm_m[w][h]);
+                for (int x = 16; x; x >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float f = wm == -INFINITY ? 0.f : ex2(wm - top);
+                float sum_l = wl != wl ? wl : wl * f;   // (without a maximum a NaN sum stays one)
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    f[w] = sm_m[w][h] == -INFINITY ? 0.f : ex2(sm_m[w][h] - top);
-                    sum_l += sm_l[w][h] != sm_l[w][h] ? sm_l[w][h] : sm_l[w][h] * f[w];
-                }
-                const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
-                for (int c = 4 * lane; c < D; c += 128) {
+                for (int x = 16; x; x >>= 1)
+                    sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
+                const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+#pragma unroll
+                for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
+                    const int c = min(4 * lane + 128 * q, DP - 4);
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         const float4 y = *reinterpret_cast<const float4 *>(
                             smem + (w * S::kStages + stage) * S::kStage + at(h, c) * 4);
-                        x.x = fmaf(y.x, f[w], x.x), x.y = fmaf(y.y, f[w], x.y);
-                        x.z = fmaf(y.z, f[w], x.z), x.w = fmaf(y.w, f[w], x.w);
+                        const float k = __shfl_sync(0xffffffffu, f, w);
+                        x.x = fmaf(y.x, k, x.x), x.y = fmaf(y.y, k, x.y);
+                        x.z = fmaf(y.z, k, x.z), x.w = fmaf(y.w, k, x.w);
                     }
-                    if (whole)
-                        finish(h, c, x, inv);
-                    else
-                        *reinterpret_cast<float4 *>(pc.at_o(piece, h) + c) = x;
+                    if (4 * lane + 128 * q < D)
+                        put(whole, h, c, x, inv);
                 }
-                if (whole)
-                    finish_lse(h, top, sum_l);
-                else if (lane == 0)
-                    *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
+                if (lane == 0)
+                    put_sum(whole, h, top, sum_l);
             }
             if (!whole) {
-                // the blocks that hold a piece, from the one with the unit's
-                // first tile (its second piece) to the one with its last
-                // (their first pieces), sixteen to a bunch
-                const int c0 = (int)(((ubeg + 1) * G + total - 1) / total - 1);
-                const int c1 = (int)((uend * G + total - 1) / total - 1);
-                const int bunches = (c1 - c0) / kFan + 1, bunch = ((int)blockIdx.x - c0) / kFan;
-                const int b0 = c0 + bunch * kFan, count = min(kFan, c1 - b0 + 1);
+                // A unit's pieces: the second of the block with its first tile,
+                // the first of the others.  kFan of them are joined by their
+                // last block, into the first of them if there are more; those
+                // by their last block.
+                const int c0 = split.block_of(ubeg), c1 = split.block_of(uend - 1);
                 auto piece_of = [&](int b) { return 2 * (int64_t)b + (b == c0 ? 1 : 0); };
-                auto arrive = [&](uint32_t *ctr, int of) {   // whether this block is the last of `of`
-                    __threadfence();
-                    __syncthreads();
+                const int bunches = (c1 - c0) / kFan + 1, b0 = c0 + ((int)blockIdx.x - c0) / kFan * kFan;
+                piece = piece_of(b0);
+#pragma unroll 1
+                for (int level = 0; level < 2; ++level) {
+                    const int first = level ? c0 : b0, step = level ? kFan : 1;
+                    const int count = level ? bunches : min(kFan, c1 - b0 + 1);
+                    const bool out = level || bunches == 1;
+                    __syncthreads();   // (the block's writes, ordered by the fence before the count)
                     if (tid == 0) {
-                        const bool is = atomicAdd(ctr, 1u) == (uint32_t)of - 1;
-                        if (is)
-                            *ctr = 0;
-                        last = is;
+                        uint32_t *c = level ? ctr + 2 * kMaxCtas + c0 : ctr + piece;
+                        __threadfence();
+                        last = atomicAdd(c, 1u) == (uint32_t)count - 1;
+                        if (last)
+                            *c = 0;
+                        __threadfence();
                     }
                     __syncthreads();
                     if (!last)
-                        return false;
-                    __threadfence();
-                    return true;
-                };
-                auto join_all = [&](int count, auto from, bool out) {
+                        break;
+#pragma unroll 1
                     for (int h = warp; h < heads; h += W) {
-                        float4 x[DP > 128 ? 2 : 1];
-                        float top, sum_l;
-                        join<DP>(pc, count, h, from, x, top, sum_l);
-                        const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+                        // lane i has maximum and sum of pieces i, i + 32, i + 64
+                        float pm[kFan / 32], f[kFan / 32], top = -INFINITY, sum_l = 0.f;
+                        float2 ml[kFan / 32];
 #pragma unroll
-                        for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
-                            const int c = 4 * lane + 128 * q;
-                            if (c >= D)
-                                continue;
-                            if (out)
-                                finish(h, c, x[q], inv);
-                            else
-                                *reinterpret_cast<float4 *>(pc.at_o(piece_of(b0), h) + c) = x[q];
+                        for (int k = 0; k < kFan / 32; ++k)
+                            ml[k] = lane + 32 * k < count
+                                        ? __ldcg(reinterpret_cast<const float2 *>(
+                                              pc.at_ml(piece_of(first + (lane + 32 * k) * step), h)))
+                                        : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                        for (int k = 0; k < kFan / 32; ++k)
+                            pm[k] = ml[k].x, top = fmaxf(top, pm[k]);
+#pragma unroll
+                        for (int x = 16; x; x >>= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+#pragma unroll
+                        for (int k = 0; k < kFan / 32; ++k) {
+                            f[k] = pm[k] == -INFINITY ? 0.f : ex2(pm[k] - top);
+                            sum_l += ml[k].y != ml[k].y ? ml[k].y : ml[k].y * f[k];
                         }
-                        if (out)
-                            finish_lse(h, top, sum_l);
-                        else if (lane == 0)
-                            *reinterpret_cast<float2 *>(pc.at_ml(piece_of(b0), h)) = make_float2(top, sum_l);
+#pragma unroll
+                        for (int x = 16; x; x >>= 1)
+                            sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
+                        const float inv = !out ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+#pragma unroll 1
+                        for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
+                            const int c = min(4 * lane + 128 * q, DP - 4);
+                            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int k = 0; k < kFan / 32; ++k) {
+#pragma unroll 1
+                                for (int i = 0; i < 32 && 32 * k + i < count; i += kBatch) {
+                                    float4 y[kBatch];
+#pragma unroll
+                                    for (int z = 0; z < kBatch; ++z)
+                                        y[z] = 32 * k + i + z < count
+                                                   ? __ldcg(reinterpret_cast<const float4 *>(
+                                                         pc.at_o(piece_of(first + (32 * k + i + z) * step), h) + c))
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                    for (int z = 0; z < kBatch; ++z) {
+                                        const float w = __shfl_sync(0xffffffffu, f[k], i + z);
+                                        x.x = fmaf(y[z].x, w, x.x), x.y = fmaf(y[z].y, w, x.y);
+                                        x.z = fmaf(y[z].z, w, x.z), x.w = fmaf(y[z].w, w, x.w);
+                                    }
+                                }
+                            }
+                            if (4 * lane + 128 * q < D)
+                                put(out, h, c, x, inv);
+                        }
+                        if (lane == 0)
+                            put_sum(out, h, top, sum_l);
                     }
-                };
-                if (arrive(ctr + piece_of(b0), count)) {
-                    join_all(count, [&](int i) { return piece_of(b0 + i); }, bunches == 1);
-                    if (bunches > 1 && arrive(ctr + 2 * kMaxCtas + c0, bunches))
-                        join_all(bunches, [&](int i) { return piece_of(c0 + i * kFan); }, true);
+                    if (out)
+                        break;
                 }
             }
             __syncthreads();   // the stages and sums are read
             fresh = true;
         }
-        use.next(a, units);
+        use.next(a);
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
+    clear_rows();
+}
+
+// Keys that a row of the block table can name.
+int64_t key_cap(int64_t max_pages, int64_t page_size)
+{
+    const int64_t n = max_pages * page_size;
+    return n < INT32_MAX ? n : INT32_MAX;
 }
 
 int padded(int64_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
 template <int DT, int DP>
-cudaError_t launch(const PagedAttention &a, uint32_t *err, cudaStream_t stream)
+cudaError_t launch(const PagedAttention &p, uint32_t *err, cudaStream_t stream)
 {
     using S = Shape<DT, DP>;
-    auto *k = k_paged_attention<DT, DP>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static_assert(S::kTile >= kMinTile, "tile bound");
+    auto *kernel = k_paged_attention<DT, DP>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     int dev = 0, sms = 0;
     if (e == cudaSuccess)
         e = cudaGetDevice(&dev);
@@ -858,16 +913,33 @@ cudaError_t launch(const PagedAttention &a, uint32_t *err, cudaStream_t stream)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
+    const tw_kv_cache &c = p.cache;
+    Args a{};
+    a.q = p.q, a.out = p.out, a.lse = p.lse, a.table = p.block_table, a.lengths = p.lengths, a.first = p.first;
+    a.k = static_cast<const uint8_t *>(c.k);
+    a.v_of_k = static_cast<const uint8_t *>(c.v) - a.k;
+    a.k_scale = c.k_scale, a.v_scale = c.v_scale, a.ws = p.ws, a.err = err;
+    a.ldq = p.ldq, a.ldo = p.ldo, a.table_stride = p.table_stride;
+    a.page_bytes = c.page_stride * S::kElem, a.row_bytes = c.token_stride * S::kElem;
+    a.head_bytes = c.head_stride * S::kElem;
+    a.requests = (int)p.requests, a.heads = p.heads, a.kv_heads = (int)c.kv_heads, a.group = a.heads / a.kv_heads;
+    a.per_kv = (int)ceil_div(a.group, kHeads), a.units = a.kv_heads * a.per_kv;
+    a.D = (int)c.head_dim, a.P = (int)c.page_size, a.pages = (int)c.num_pages;
+    a.page_shift = -1;
+    for (int b = 0; b < 31; ++b)
+        if (a.P == 1 << b)
+            a.page_shift = b;
+    a.cap = (int)key_cap(p.max_pages, c.page_size);
+    a.short_way = a.P % kKeys == 0 && ((a.page_bytes | a.row_bytes | a.head_bytes) >> 32) == 0;
+    a.mul = p.scale * kLog2e;
     // As many blocks as are resident; no more than tiles that the block table
     // can hold.
-    const int64_t group = a.heads / a.cache.kv_heads;
-    const int64_t units = a.cache.kv_heads * ceil_div(group, kHeads);
-    const int64_t span = a.max_pages * a.cache.page_size;
-    const int64_t tiles = a.requests * units * ceil_div(span < INT32_MAX ? span : INT32_MAX, S::kTile);
+    const int64_t tiles = p.requests * a.units * ceil_div(a.cap, S::kTile);
     int64_t grid = (int64_t)sms * S::kBlocks;
     grid = grid < kMaxCtas ? grid : kMaxCtas;
+    static_assert(kFan * kFan >= kMaxCtas, "two joins at most");
     grid = grid < tiles ? grid : tiles;
-    k<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a, err);
+    kernel<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -882,6 +954,12 @@ cudaError_t launch_type(const PagedAttention &a, uint32_t *err, cudaStream_t str
 }
 
 }  // namespace
+
+bool paged_attention_fits(int64_t requests, int64_t heads, int64_t kv_heads, int64_t max_pages, int64_t page_size)
+{
+    return requests * kv_heads * ceil_div(heads / kv_heads, kHeads) *
+               ceil_div(key_cap(max_pages, page_size), kMinTile) <= INT32_MAX;
+}
 
 // Counters (one per piece, one per block), then maxima and sums, then sums of
 // values of two pieces per block: the first and the last of its run.

@@ -110,6 +110,9 @@ int check_attention(const tw::PagedAttention &p, size_t ws_bytes, const char *wh
         p.table_stride > INT32_MAX)
         return fail(TW_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", who,
                     (long long)p.max_pages, (long long)p.table_stride);
+    if (!tw::paged_attention_fits(p.requests, p.heads, p.cache.kv_heads, p.max_pages, p.cache.page_size))
+        return fail(TW_ERR_SHAPE, "%s: %lld requests with tables of %lld pages are too many for one call", who,
+                    (long long)p.requests, (long long)p.max_pages);
     if (!std::isfinite(p.scale))
         return fail(TW_ERR_NONFINITE, "%s: scale is not finite", who);
     if (overlap(p.q, 4 * ((p.requests - 1) * p.ldq + p.heads * D), p.out,

@@ -157,6 +157,9 @@ struct PagedAttention {
     uint8_t *ws;
 };
 int64_t paged_attention_ws_bytes(int64_t head_dim);
+// Whether the tiles of such a call, were every table row full, can be counted in 31 bits.
+bool paged_attention_fits(int64_t requests, int64_t heads, int64_t kv_heads, int64_t max_pages,
+                          int64_t page_size);
 cudaError_t launch_paged_attention(const PagedAttention &a, uint32_t *err, cudaStream_t stream);
 
 // ------------------------------------------------------- residual and norms

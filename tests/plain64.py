@@ -59,7 +59,7 @@ def rotate(x, positions, inv_freq, interleaved):
     return out, tol
 
 
-def attention(q, k, v, scale, heads):
+def attention(q, k, v, scale, heads, v_scale=None):
     """One request: q [heads, d], k and v [n, kv_heads, d] in 64 bits.  Returns
     out, lse and their bounds.
 
@@ -71,7 +71,13 @@ def attention(q, k, v, scale, heads):
     (2^-21, the rescalings with it), and carried in 21 bits (2^-22); the sums
     over n keys add n roundings at most (2^-24 each).  All of that relative to
     sum p |v|; the division adds one rounding, the sum of weights the same
-    errors again."""
+    errors again.
+
+    fp16 operands end at 2^-24.  The largest weight is carried at 2^12 or
+    more, so that any weight is off by half of fp16's last step at most: by
+    2^-25 / 2^12 = 2^-37 of the largest, for each key times its value.  Over
+    codes it is weight times v_scale [n, kv_heads] that is carried, to 2^-37
+    of its largest, times the code."""
     n = k.shape[0]
     group = heads // k.shape[1] if k.ndim == 3 else 1
     d = q.shape[1]
@@ -87,7 +93,9 @@ def attention(q, k, v, scale, heads):
         e = abs(scale) * (np.abs(kk) @ np.abs(q[h])).max() * (2.0 ** -22 + (d + 2) * 2.0 ** -24) \
             + 2.0 ** -23 * np.abs(s).max()
         rel = 2 * e + 2.0 ** -21 + 2.0 ** -22 + n * 2.0 ** -24
-        out_tol[h] = 2 * rel * ((p / p.sum()) @ np.abs(vv)) + 1e-38
+        vs = np.ones(n) if v_scale is None else np.where(v_scale[:, h // group] > 0, v_scale[:, h // group], 1.0)
+        tiny = 2.0 ** -37 * (p * vs).max() * (np.abs(vv) / vs[:, None]).sum(axis=0) / p.sum()
+        out_tol[h] = 2 * rel * ((p / p.sum()) @ np.abs(vv)) + tiny + 1e-38
         lse_tol[h] = rel + 2.0 ** -23 * (abs(lse[h]) + abs(m))
     return out, lse, out_tol, lse_tol
 

@@ -77,6 +77,14 @@ def rows_of(cache, table, r, lo, hi):
     return out
 
 
+def scales_of(cache, table, r, lo, hi):
+    """The scales of the values of a request's places, or None."""
+    if cache.v_scale is None:
+        return None
+    j = np.arange(lo, hi)
+    return cache.v_scale.cpu().numpy().astype(np.float64)[table[r][j // cache.page_size], j % cache.page_size]
+
+
 def check_all(api, cache, q, table, lengths, first, out, lse, heads, scale=None):
     d = cache.head_dim
     scale = d ** -0.5 if scale is None else scale
@@ -84,7 +92,8 @@ def check_all(api, cache, q, table, lengths, first, out, lse, heads, scale=None)
     for r, n in enumerate(lengths):
         lo = 0 if first is None else min(max(first[r], 0), n)
         k, v = rows_of(cache, table, r, lo, n)
-        w, wl, tol, tl = plain64.attention(q[r].reshape(heads, d).astype(np.float64), k, v, scale, heads)
+        w, wl, tol, tl = plain64.attention(q[r].reshape(heads, d).astype(np.float64), k, v, scale, heads,
+                                           scales_of(cache, table, r, lo, n))
         got = out[r].reshape(heads, d)
         assert (np.abs(got - w) <= tol).all(), (r, n, float((np.abs(got - w) - tol).max()))
         if n > lo:
