@@ -507,6 +507,7 @@ tw_decoder_chain_cached = _sig("tw_decoder_chain_cached", _int,
 # each property of a tensor once and look for the words only to refuse it.
 _F32, _F64, _I32, _I8, _U8 = torch.float32, torch.float64, torch.int32, torch.int8, torch.uint8
 _current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+_empty_strided = torch.empty_strided
 
 
 def _launch(fn, index, stream, used, *args):
@@ -530,12 +531,12 @@ def _launch(fn, index, stream, used, *args):
                 t.record_stream(stream)
 
 
-def _new(beside, size, dtype, stream):
+def _new(beside, size, strides, dtype, stream):
     """An output on the device of ``beside``, made on the stream that writes it."""
     if stream is None:
-        return beside.new_empty(size, dtype=dtype)
+        return _empty_strided(size, strides, dtype=dtype, device=beside.device)
     with torch.cuda.stream(stream):
-        return beside.new_empty(size, dtype=dtype)
+        return _empty_strided(size, strides, dtype=dtype, device=beside.device)
 
 
 def _refuse(t, dtype, shape, name, index):
@@ -681,24 +682,23 @@ def kv_assign(lengths: torch.Tensor, delta: torch.Tensor, block_table: torch.Ten
     width, stride = _table(block_table, n, index)
     if rows < 0:
         raise ValueError("rows must be >= 0")
-    if lengths_out is None:
-        lengths_out = _new(lengths, (n,), _I32, stream)
-    else:
+    if lengths_out is not None:
         _vector(lengths_out, _I32, n, "lengths_out", index)
-    if free_count_out is None:
-        free_count_out = _new(lengths, (1,), _I32, stream)
-    else:
+    if free_count_out is not None:
         _vector(free_count_out, _I32, 1, "free_count_out", index)
-    per_row = _new(lengths, (3, rows), _I32, stream)
-    slots, positions, requests = per_row.unbind(0)
-    row_start = _new(lengths, (n + 1,), _I32, stream)
-    at = per_row.data_ptr()
+    made = _new(lengths, (3 * rows + 2 * n + 2,), (1,), _I32, stream)
+    slots, positions, requests, row_start, new_lengths, new_count = made.split_with_sizes(
+        (rows, rows, rows, n + 1, n, 1))
+    if lengths_out is None:
+        lengths_out = new_lengths
+    if free_count_out is None:
+        free_count_out = new_count
+    at = made.data_ptr()
     _launch(tw_kv_assign, index, stream,
-            (lengths, delta, block_table, free_pages, free_count, lengths_out, free_count_out, per_row,
-             row_start),
+            (lengths, delta, block_table, free_pages, free_count, lengths_out, free_count_out, made),
             lengths.data_ptr(), delta.data_ptr(), n, page_size, block_table.data_ptr(), width, stride,
             free_pages.data_ptr(), capacity, free_count.data_ptr(), lengths_out.data_ptr(),
-            free_count_out.data_ptr(), at, at + 4 * rows, at + 8 * rows, rows, row_start.data_ptr())
+            free_count_out.data_ptr(), at, at + 4 * rows, at + 8 * rows, rows, at + 12 * rows)
     return KVAssignment(lengths_out, free_count_out, slots, positions, requests, row_start)
 
 
@@ -728,7 +728,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
         rotary, freq = 2 * len(inv_freq), inv_freq.data_ptr()
         _vector(inv_freq, _F64, rotary // 2, "inv_freq", index)
     if q_out is None:
-        q_out = _new(q, (rows, width), _F32, stream)
+        q_out = _new(q, (rows, width), (width, 1), _F32, stream)
         ldqo = width
     else:
         ldqo = _rows(q_out, rows, width, "q_out", index)
@@ -769,7 +769,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     if first is not None:
         _vector(first, _I32, n, "first", index)
     if out is None:
-        out = _new(q, (n, width), _F32, stream)
+        out = _new(q, (n, width), (width, 1), _F32, stream)
         ldo = width
     else:
         ldo = _rows(out, n, width, "out", index)
@@ -778,7 +778,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                 lse.shape != (n, heads) or not lse.is_contiguous():
             _refuse(lse, _F32, (n, heads), "lse", index)
     elif return_lse:
-        lse = _new(q, (n, heads), _F32, stream)
+        lse = _new(q, (n, heads), (heads, 1), _F32, stream)
     if ws is None:
         if stream is None:
             ws = paged_attention_workspace(n, heads, cache)
@@ -846,20 +846,20 @@ def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str |
     if h is not None:
         ldh = _rows(h, rows, width, "h", index)
     elif y is not None:
-        h = _new(x, size, _F32, stream)
+        h = _new(x, size, (width, 1), _F32, stream)
         ldh = width
     # (neither: h is x as it stands)
     xq = amax = qsum = None
     if quantize:
         if n is not None:
             raise ValueError("quantize gives codes: n cannot be passed in")
-        xq = _new(x, size, _I8, stream)
-        amax = _new(x, (rows,), _F32, stream)
-        qsum = _new(x, (rows,), _I32, stream)
+        xq = _new(x, size, (width, 1), _I8, stream)
+        amax = _new(x, (rows,), (1,), _F32, stream)
+        qsum = _new(x, (rows,), (1,), _I32, stream)
     elif n is not None:
         ldn = _rows(n, rows, width, "n", index)
     elif pre is not None:
-        n = _new(x, size, _F32, stream)
+        n = _new(x, size, (width, 1), _F32, stream)
         ldn = width
     elif h is None:
         raise ValueError("nothing to compute: no y, no norm and no codes")

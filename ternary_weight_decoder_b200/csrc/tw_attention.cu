@@ -14,8 +14,8 @@
 // to end, and every block takes an equal run of them, whatever the lengths
 // are.  A block whose run holds all of a (request, KV head) writes its
 // output; the pieces of one that spans blocks go to the workspace and are
-// joined in a fixed order, by the last block of every kFan and then by the
-// last of those.  Inside a block each warp takes 16 keys of every tile
+// joined in a fixed order, each head by the warp that finishes it last, kFan
+// pieces at a time and then those.  Inside a block each warp takes 16 keys of every tile
 // through its own ring of cp.async stages: no barrier until a piece ends.
 //
 // Matrix products: the 16 keys (or 16 columns of the values) are the rows of
@@ -26,6 +26,7 @@
 // digits (23 bits of the head's largest), whose products are exact integers.
 // Scores and sums are fp32.
 // Groups of more than eight heads are split into units of eight.
+#include <atomic>
 #include <cfloat>
 
 #include "tw_kv.cuh"
@@ -35,6 +36,9 @@
 #endif
 #ifndef TW_ATT_WARPS_CODES
 #define TW_ATT_WARPS_CODES 12
+#endif
+#ifndef TW_ATT_HALVES
+#define TW_ATT_HALVES 2
 #endif
 #ifndef TW_ATT_RUN
 #define TW_ATT_RUN 2
@@ -49,11 +53,9 @@
 namespace tw {
 namespace {
 
-constexpr int kKeys = 16;                    // keys of a warp's step
 constexpr int kMaxCtas = 512;                // counters and partial results in the workspace
 constexpr int kHeads = 8;                    // query heads of a unit
-constexpr int kBatch = 16;                   // of them at a time
-constexpr int kFan = 96;                     // pieces that one block joins
+constexpr int kFan = 16;                     // pieces that one warp joins, of one head
 constexpr int kMinTile = 32;                 // keys of the smallest variant's tile
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
@@ -86,6 +88,11 @@ struct Shape {
     static constexpr int kElem = kCodes ? 1 : 2;
     static constexpr int kRow = DP * kElem;            // bytes of a key
     static constexpr int kChunks = kRow / 16;
+    // Keys of a warp's step: twice 16 of codes, so that a step moves as many
+    // bytes and its fixed instructions count for as little as of 16 bits.
+    static constexpr int kHalves = kCodes ? TW_ATT_HALVES : 1;
+    static constexpr int kKeys = 16 * kHalves;
+    static constexpr uint32_t kAll = kHalves == 2 ? 0xffffffffu : 0xffffu;
     static constexpr int kPool = kKeys * kRow;         // bytes of a step's keys
     static constexpr int kStage = 2 * kPool;
     static constexpr int kScales = kCodes ? 2 * kKeys * 4 : 0;   // of a stage, behind the rings
@@ -228,21 +235,32 @@ template <int TILE>
 struct Cursor {
     int r, u, t;
     Span s;
-    __device__ __forceinline__ void next(const Args &a)
+    // One tile on; whether that is another unit.
+    __device__ __forceinline__ bool next(const Args &a)
     {
         if (++t < s.tiles)
-            return;
+            return false;
         t = 0;
         if (++u < a.units)
-            return;
+            return true;
         u = 0;
         do {
             if (++r >= a.requests)
-                return;
+                return true;
             s = span_of<TILE>(a, r);
         } while (s.tiles == 0);
+        return true;
     }
 };
+
+// Count one up at device scope, ordering what this thread has seen written
+// before it and what it reads after it.
+__device__ __forceinline__ uint32_t count_up(uint32_t *ctr)
+{
+    uint32_t was;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(was) : "l"(ctr) : "memory");
+    return was;
+}
 
 // The pieces of one unit in the workspace: maxima and sums [piece][head][2],
 // sums of values [piece][head][DP].
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
 {
     using S = Shape<DT, DP>;
     constexpr bool BF = S::kBf;
-    constexpr int W = S::kWarps, kThreads = S::kThreads, kTile = S::kTile;
+    constexpr int W = S::kWarps, H = S::kHalves, kThreads = S::kThreads, kTile = S::kTile;
     // The running maximum is raised once a score passes it by this much (in
     // powers of two), so that most steps leave the sums alone.  Weights are
     // then up to 2^slack; fp16 ones are carried times 2^12 (as is the sum),
@@ -282,7 +300,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     constexpr float kSlack = BF ? 8.f : 3.f, kUp = BF ? 0.f : 12.f;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t part[W];
-    __shared__ int start[3], last;
+    __shared__ int start[3];
     __shared__ uint32_t bounds[2];
     __shared__ float sm_m[W][kHeads], sm_l[W][kHeads], sm_back[kHeads];
     __shared__ uint32_t sm_mask[W][S::kStages];
@@ -380,89 +398,113 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
 
     // ---- the ring of stages
     constexpr int kRowsPer = S::kChunks >= 32 ? 1 : 32 / S::kChunks;   // rows of one pass of the warp
+    constexpr bool kWide = S::kChunks >= 32;                           // a pass is a row: all lanes stay in step
     const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
     const uint32_t scales = smem_u32(smem) + W * S::kStages * S::kStage + warp * S::kStages * S::kScales;
     const int row0 = lane / S::kChunks, chunk = lane % S::kChunks;
     const uint32_t lane_dst = ring + place<S::kChunks>(row0, chunk);
-    const uint8_t *kpool = a.k + row0 * a.row_bytes + chunk * 16;
-    const float *scale_pool = (lane < 16 ? a.k_scale : a.v_scale) + (lane & 15) * a.kv_heads;
     const bool in_row = chunk < D * S::kElem / 16;
-    // The next step's first key and, if its keys are visible and share a page
-    // (the short way), that page: looked up a step early.
-    int next_j = 0, next_in = 0, next_page = -1;
+    // Of the unit that is being fetched: its table row, its head's pools.
+    const int32_t *table;
+    const uint8_t *kpool;
+    int head;
+    auto enter_unit = [&] {
+        head = load.u / a.per_kv;
+        table = a.table + load.r * a.table_stride;
+        kpool = a.k + head * a.head_bytes + row0 * a.row_bytes + chunk * 16;
+    };
+    // The next step's first key and, for every 16 keys that are visible and
+    // share a page (the short way), that page: looked up a step early.
+    int next_j = 0, next_in[H] = {}, next_page[H];
     auto look_up = [&] {
-        next_j = (load.s.first_tile + load.t) * kTile + warp * kKeys;
-        next_page = -1;
-        if (a.short_way && next_j >= load.s.lo && next_j + kKeys <= load.s.hi) {
-            const int p = a.page_shift >= 0 ? next_j >> a.page_shift : next_j / a.P;
-            next_in = next_j - p * a.P;
-            next_page = __ldg(a.table + load.r * a.table_stride + p);
+        next_j = (load.s.first_tile + load.t) * kTile + warp * S::kKeys;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int j = next_j + 16 * h;
+            next_page[h] = -1;
+            if (a.short_way && j >= load.s.lo && j + 16 <= load.s.hi) {
+                const int p = a.page_shift >= 0 ? j >> a.page_shift : j / a.P;
+                next_in[h] = j - p * a.P;
+                next_page[h] = __ldg(table + p);
+            }
         }
     };
-    uint32_t partial = 0;   // stages filled the long way: their masks are in sm_mask
+    uint32_t partial = 0;   // stages with keys left out: their masks are in sm_mask
     auto fetch = [&](int stage) {
-        const int head = load.u / a.per_kv;
         const uint32_t base = stage * S::kStage;
-        if ((uint32_t)next_page < (uint32_t)a.pages) {
-            const uint8_t *ks = kpool + (uint64_t)(uint32_t)next_page * (uint32_t)a.page_bytes +
-                                (uint64_t)(uint32_t)next_in * (uint32_t)a.row_bytes +
-                                (uint64_t)(uint32_t)head * (uint32_t)a.head_bytes;
-            const uint8_t *vs = ks + a.v_of_k;
-            if (DP * S::kElem >= 512 || in_row) {
+        uint32_t mask = 0;
+        int64_t slot = -1;   // codes: this lane's key
+        auto half = [&](int h, int page0, int in0) {
+            const uint32_t rows = base + h * 16 * S::kRow;
+            if ((uint32_t)page0 < (uint32_t)a.pages) {
+                const uint8_t *ks = kpool + (uint64_t)(uint32_t)page0 * (uint32_t)a.page_bytes +
+                                    (uint64_t)(uint32_t)in0 * (uint32_t)a.row_bytes;
+                const uint8_t *vs = ks + a.v_of_k;
+                mask |= 0xffffu << (16 * h);
+                if (S::kCodes && (lane >> 4) == h)
+                    slot = (uint32_t)(page0 * a.P + in0) + (lane & 15);
+                if (kWide || in_row) {
 #pragma unroll
-                for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                    const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
-                    cp_async16(dst + kRowsPer * i * S::kRow, DP * S::kElem < 512 || in_row ? ks : a.k,
-                               DP * S::kElem < 512 || in_row);
-                    cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, DP * S::kElem < 512 || in_row ? vs : a.k,
-                               DP * S::kElem < 512 || in_row);
-                    ks += kRowsPer * a.row_bytes, vs += kRowsPer * a.row_bytes;
-                }
-            } else {   // past head_dim: zeros
+                    for (int i = 0; i < 16 / kRowsPer; ++i) {
+                        const uint32_t dst = (lane_dst + rows) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
+                        cp_async16(dst + kRowsPer * i * S::kRow, !kWide || in_row ? ks : a.k, !kWide || in_row);
+                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, !kWide || in_row ? vs : a.k,
+                                   !kWide || in_row);
+                        ks += kRowsPer * a.row_bytes, vs += kRowsPer * a.row_bytes;
+                    }
+                } else {   // past head_dim: zeros
 #pragma unroll 1
-                for (int i = 0; i < kKeys / kRowsPer; ++i) {
-                    const uint32_t dst = (lane_dst + base) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
-                    cp_async16(dst + kRowsPer * i * S::kRow, a.k, false);
-                    cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, a.k, false);
+                    for (int i = 0; i < 16 / kRowsPer; ++i) {
+                        const uint32_t dst = (lane_dst + rows) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
+                        cp_async16(dst + kRowsPer * i * S::kRow, a.k, false);
+                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, a.k, false);
+                    }
+                }
+                return;
+            }
+            const int j = next_j + 16 * h + (lane & 15);
+            bool ok = j >= load.s.lo && j < load.s.hi;
+            int64_t off = 0;
+            if (ok) {
+                const int p = j / a.P;
+                const int page = __ldg(table + p);
+                if ((uint32_t)page < (uint32_t)a.pages) {
+                    const int in = j - p * a.P;
+                    off = page * a.page_bytes + in * a.row_bytes;
+                    if (S::kCodes && (lane >> 4) == h)
+                        slot = (int64_t)page * a.P + in;
+                } else {
+                    ok = false;
+                    atomicOr(a.err, EFLAG_BADDESC);
                 }
             }
-            if (S::kCodes)
-                cp_async4(scales + stage * S::kScales + lane * 4,
-                          scale_pool + (uint64_t)(uint32_t)(next_page * a.P + next_in) * (uint32_t)a.kv_heads + head,
-                          true);
-            partial &= ~(1u << stage);
-            return;
-        }
-        const int j = next_j + (lane & 15);
-        bool ok = j >= load.s.lo && j < load.s.hi;
-        int64_t off = 0, slot = 0;
-        if (ok) {
-            const int p = j / a.P;
-            const int page = __ldg(a.table + load.r * a.table_stride + p);
-            if ((uint32_t)page < (uint32_t)a.pages) {
-                const int in = j - p * a.P;
-                off = page * a.page_bytes + in * a.row_bytes + head * a.head_bytes;
-                slot = ((int64_t)page * a.P + in - (lane & 15)) * a.kv_heads + head;
-            } else {
-                ok = false;
-                atomicOr(a.err, EFLAG_BADDESC);
-            }
-        }
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-        if (lane == 0)
-            sm_mask[warp][stage] = mask;
-        partial |= 1u << stage;
+            const uint32_t some = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+            mask |= some << (16 * h);
 #pragma unroll 1
-        for (int i = 0; i < kKeys / kRowsPer; ++i) {
-            const int row = row0 + kRowsPer * i;
-            const int64_t o = __shfl_sync(0xffffffffu, off, row) - row0 * a.row_bytes;
-            const bool in = ((mask >> row) & 1) && in_row;
-            const uint32_t dst = ring + base + place<S::kChunks>(row, chunk);
-            cp_async16(dst, in ? kpool + o : a.k, in);
-            cp_async16(dst + S::kPool, in ? kpool + a.v_of_k + o : a.k, in);
+            for (int i = 0; i < 16 / kRowsPer; ++i) {
+                const int row = row0 + kRowsPer * i;
+                const int64_t o = __shfl_sync(0xffffffffu, off, row) - row0 * a.row_bytes;
+                const bool in = ((some >> row) & 1) && in_row;
+                const uint32_t dst = ring + rows + place<S::kChunks>(row, chunk);
+                cp_async16(dst, in ? kpool + o : a.k, in);
+                cp_async16(dst + S::kPool, in ? kpool + a.v_of_k + o : a.k, in);
+            }
+        };
+        half(0, next_page[0], next_in[0]);
+        if constexpr (H == 2)
+            half(1, next_page[H - 1], next_in[H - 1]);
+        if (S::kCodes) {
+            const uint32_t dst = scales + stage * S::kScales + lane * 4;
+            const int64_t at = slot < 0 ? 0 : slot * a.kv_heads + head;
+            cp_async4(dst, a.k_scale + at, slot >= 0);
+            cp_async4(dst + S::kKeys * 4, a.v_scale + at, slot >= 0);
         }
-        if (S::kCodes)
-            cp_async4(scales + stage * S::kScales + lane * 4, ok ? scale_pool + slot : a.k_scale, ok);
+        partial &= ~(1u << stage);
+        if (mask != S::kAll) {
+            partial |= 1u << stage;
+            if (lane == 0)
+                sm_mask[warp][stage] = mask;
+        }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
@@ -474,6 +516,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     const int n = (int)(end - begin);
     int stage = 0;
     bool fresh = true;
+    enter_unit();
     look_up();
 #pragma unroll 1
     for (int i = 1 - S::kStages; i < n; ++i) {
@@ -484,9 +527,11 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         }
         if (i + S::kStages - 1 < n) {
             fetch(i < 0 ? i + S::kStages - 1 : stage == 0 ? S::kStages - 1 : stage - 1);
-            load.next(a);
-            if (i + S::kStages < n)
+            if (i + S::kStages < n) {
+                if (load.next(a))
+                    enter_unit();
                 look_up();
+            }
         }
         commit();
         if (i < 0)
@@ -579,88 +624,112 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         }
 
         const uint32_t base = ring + stage * S::kStage;
-        const uint32_t mask = (partial >> stage) & 1 ? sm_mask[warp][stage] : 0xffffu;
+        const uint32_t mask = (partial >> stage) & 1 ? sm_mask[warp][stage] : S::kAll;
         if (mask) {
-            // ---- scores of keys g, g + 8 for heads 2 t4, 2 t4 + 1
+            // ---- scores of keys g, g + 8 of 16 for heads 2 t4, 2 t4 + 1
             // (keys 0-7, 8-15) x (16 bytes at chunk 2 j, at 2 j + 1)
             const uint32_t kbase = base + place<S::kChunks>(lane & 15, lane >> 4);
-            float sc[4];
+            float s[H][4];
             if constexpr (S::kCodes) {
-                int acc[S::kQueryParts][4] = {};
+                int acc[H][3][4];
 #pragma unroll
                 for (int j = 0; j < S::kQuerySteps; ++j) {
-                    uint32_t f[4];
-                    ldmatrix4<false>(f, kbase ^ (j << 5));
+                    uint32_t f[H][4];
 #pragma unroll
-                    for (int k = 0; k < S::kQueryParts; ++k) {
-                        const uint2 v = qs[(j * S::kQueryParts + k) * 32 + lane];
-                        mma_s8_16832(acc[k], f[0], f[1], f[2], f[3], v.x, v.y);
+                    for (int h = 0; h < H; ++h)
+                        ldmatrix4<false>(f[h], (kbase + h * 16 * S::kRow) ^ (j << 5));
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const uint2 v = qs[(j * 3 + k) * 32 + lane];
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            if (j == 0)
+                                acc[h][k][0] = acc[h][k][1] = acc[h][k][2] = acc[h][k][3] = 0;
+                            mma_s8_16832(acc[h][k], f[h][0], f[h][1], f[h][2], f[h][3], v.x, v.y);
+                        }
                     }
                 }
                 // exact sums of each digit (below 2^23); one rounding each below
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sc[e] = fmaf((float)(acc[0][e] * 256 + acc[1][e]), 256.f, (float)acc[2][e]);
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[h][e] = fmaf((float)(acc[h][0][e] * 256 + acc[h][1][e]), 256.f, (float)acc[h][2][e]) *
+                                  unscale[e & 1];
             } else {
-                float acc[S::kQueryParts][4] = {};
+                float acc[H][S::kQueryParts][4];
 #pragma unroll
                 for (int j = 0; j < S::kQuerySteps; ++j) {
-                    uint32_t f[4];
-                    ldmatrix4<false>(f, kbase ^ (j << 5));
+                    uint32_t f[H][4];
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        ldmatrix4<false>(f[h], (kbase + h * 16 * S::kRow) ^ (j << 5));
 #pragma unroll
                     for (int k = 0; k < S::kQueryParts; ++k) {
                         const uint2 v = qs[(j * S::kQueryParts + k) * 32 + lane];
-                        mma<BF>(acc[k], f[0], f[1], f[2], f[3], v.x, v.y);
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            if (j == 0)
+                                acc[h][k][0] = acc[h][k][1] = acc[h][k][2] = acc[h][k][3] = 0.f;
+                            mma<BF>(acc[h][k], f[h][0], f[h][1], f[h][2], f[h][3], v.x, v.y);
+                        }
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sc[e] = acc[0][e] + acc[1][e];
-                    if (S::kQueryParts == 3)
-                        sc[e] += acc[S::kQueryParts - 1][e];
-                }
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[h][e] = acc[h][0][e] + acc[h][1][e];
+                        if (S::kQueryParts == 3)
+                            s[h][e] += acc[h][S::kQueryParts - 1][e];
+                        if (!BF)
+                            s[h][e] *= unscale[e & 1];
+                    }
             }
             // ---- running maximum and sum.  With codes the value's scale goes
             // into the weight, 2^(s_j - m) vs_j, and into the maximum, that of
             // s_j + log2 vs_j, so that weights stay within fp16 whatever the
             // scales are (the sum of 2^(s_j - m) need not: it is fp32).
-            float s[4], vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[e] = BF ? sc[e] : sc[e] * unscale[e & 1];
+            float vs[H][2], lv[H][2];
             if (S::kCodes) {
                 const float *of = reinterpret_cast<const float *>(
-                    smem + W * S::kStages * S::kStage + (warp * S::kStages + stage) * S::kScales);
+                    smem + W * S::kStages * S::kStage + (warp * S::kStages + stage) * S::kScales) + g;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float ks = of[g + 8 * k];
-                    vs[k] = of[kKeys + g + 8 * k];
-                    s[2 * k] *= ks, s[2 * k + 1] *= ks;
-                    lv[k] = vs[k] > 0.f ? __log2f(vs[k]) : 0.f;
-                }
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float ks = of[16 * h + 8 * k];
+                        s[h][2 * k] *= ks, s[h][2 * k + 1] *= ks;
+                        vs[h][k] = of[S::kKeys + 16 * h + 8 * k];
+                        lv[h][k] = vs[h][k] > 0.f ? __log2f(vs[h][k]) : 0.f;
+                    }
             }
-            if (mask != 0xffffu) {
+            if (mask != S::kAll) {
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[h][e] = (mask >> (16 * h + g + 8 * (e >> 1))) & 1 ? s[h][e] : -INFINITY;
+            }
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[e] = (mask >> (g + 8 * (e >> 1))) & 1 ? s[e] : -INFINITY;
-            }
-            float top[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                top[h] = S::kCodes ? fmaxf(s[h] + lv[0], s[2 + h] + lv[1]) : fmaxf(s[h], s[2 + h]);
+                    top[e & 1] = fmaxf(top[e & 1], S::kCodes ? s[h][e] + lv[h][e >> 1] : s[h][e]);
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+                for (int e = 0; e < 2; ++e)
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], x));
             if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
                 float f[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float up = fmaxf(top[h], m[h]);
-                    f[h] = up == -INFINITY ? 1.f : ex2(m[h] - up);
-                    m[h] = up;
-                    l[h] *= f[h];
+                for (int e = 0; e < 2; ++e) {
+                    const float up = fmaxf(top[e], m[e]);
+                    f[e] = up == -INFINITY ? 1.f : ex2(m[e] - up);
+                    m[e] = up;
+                    l[e] *= f[e];
                 }
 #pragma unroll
                 for (int c = 0; c < S::kSteps; ++c)
@@ -669,19 +738,22 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                         o[c][e] *= f[e & 1];
             }
             const float shift[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - kUp, (m[1] == -INFINITY ? 0.f : m[1]) - kUp};
-            float p[4];
+            uint32_t w[H][S::kParts][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[e] = ex2(s[e] - shift[e & 1]);
-                l[e & 1] += p[e];
-                if (S::kCodes)
-                    p[e] *= vs[e >> 1];
-            }
-            uint32_t w[S::kParts][2];
+            for (int h = 0; h < H; ++h) {
+                float p[4];
 #pragma unroll
-            for (int k = 0; k < S::kParts; ++k) {
-                w[k][0] = transpose8(split2<BF>(p[0], p[1]));
-                w[k][1] = transpose8(split2<BF>(p[2], p[3]));
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2(s[h][e] - shift[e & 1]);
+                    l[e & 1] += p[e];
+                    if (S::kCodes)
+                        p[e] *= vs[h][e >> 1];
+                }
+#pragma unroll
+                for (int k = 0; k < S::kParts; ++k) {
+                    w[h][k][0] = transpose8(split2<BF>(p[0], p[1]));
+                    w[h][k][1] = transpose8(split2<BF>(p[2], p[3]));
+                }
             }
             // ---- weighted values: columns x heads
             if constexpr (S::kCodes) {
@@ -689,30 +761,34 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 // c, c + 1; even columns are the MMA's rows 0-7, odd ones 8-15
                 const uint32_t vbase = base + S::kPool + place<S::kChunks>(lane & 15, lane >> 4);
 #pragma unroll
-                for (int c = 0; c < S::kSteps; c += 2) {
-                    uint32_t f[4];
-                    ldmatrix4<true>(f, vbase ^ (c << 4));
+                for (int c = 0; c < S::kSteps; c += 2)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t a0 = codes2<false>(f[2 * q]), a1 = codes2<true>(f[2 * q]);
-                        const uint32_t a2 = codes2<false>(f[2 * q + 1]), a3 = codes2<true>(f[2 * q + 1]);
+                    for (int h = 0; h < H; ++h) {
+                        uint32_t f[4];
+                        ldmatrix4<true>(f, (vbase + h * 16 * S::kRow) ^ (c << 4));
 #pragma unroll
-                        for (int k = 0; k < S::kParts; ++k)
-                            mma<BF>(o[c + q], a0, a1, a2, a3, w[k][0], w[k][1]);
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t a0 = codes2<false>(f[2 * q]), a1 = codes2<true>(f[2 * q]);
+                            const uint32_t a2 = codes2<false>(f[2 * q + 1]), a3 = codes2<true>(f[2 * q + 1]);
+#pragma unroll
+                            for (int k = 0; k < S::kParts; ++k)
+                                mma<BF>(o[c + q], a0, a1, a2, a3, w[h][k][0], w[h][k][1]);
+                        }
                     }
-                }
             } else {
                 // (columns 0-7, 8-15) x (keys 0-7, 8-15)
                 const uint32_t vbase = base + S::kPool +
                                        place<S::kChunks>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 #pragma unroll
-                for (int c = 0; c < S::kSteps; ++c) {
-                    uint32_t f[4];
-                    ldmatrix4<true>(f, vbase ^ (c << 5));
+                for (int c = 0; c < S::kSteps; ++c)
 #pragma unroll
-                    for (int k = 0; k < S::kParts; ++k)
-                        mma<BF>(o[c], f[0], f[1], f[2], f[3], w[k][0], w[k][1]);
-                }
+                    for (int h = 0; h < H; ++h) {
+                        uint32_t f[4];
+                        ldmatrix4<true>(f, (vbase + h * 16 * S::kRow) ^ (c << 5));
+#pragma unroll
+                        for (int k = 0; k < S::kParts; ++k)
+                            mma<BF>(o[c], f[0], f[1], f[2], f[3], w[h][k][0], w[h][k][1]);
+                    }
             }
         }
 
@@ -744,140 +820,134 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     }
                 }
             }
-            uint32_t *ctr = reinterpret_cast<uint32_t *>(a.ws);
-            Pieces<DP> pc;
-            pc.ml = reinterpret_cast<float *>(ctr + 3 * kMaxCtas);
-            pc.o = pc.ml + kMaxCtas * 2 * 2 * kHeads;
             const bool whole = unit_done && ubeg >= begin;
-            int64_t piece = 2 * (int64_t)blockIdx.x + (ubeg >= begin ? 1 : 0);
-            // ---- the warps' maxima, sums and sums of values, merged: a head to a warp
-            auto put = [&](bool out, int h, int c, float4 x, float inv) {
+            Pieces<DP> pc;
+            pc.ml = reinterpret_cast<float *>(a.ws) + 3 * kMaxCtas * kHeads;
+            pc.o = pc.ml + kMaxCtas * 2 * 2 * kHeads;
+            // Column c of head h into the output, or into a piece.
+            auto put = [&](bool out, int piece, int h, int c, float4 x, float inv) {
                 float *to = out ? a.out + use.r * a.ldo + (int64_t)(h0 + h) * D : pc.at_o(piece, h);
                 *reinterpret_cast<float4 *>(to + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
             };
-            auto put_sum = [&](bool out, int h, float top, float sum_l) {
-                if (!out)
-                    *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
-                else if (a.lse)
-                    a.lse[(int64_t)use.r * a.heads + h0 + h] =
-                        sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
+            auto put_sum = [&](bool out, int piece, int h, float top, float sum_l) {
+                if (lane == 0) {
+                    if (!out)
+                        *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
+                    else if (a.lse)
+                        a.lse[(int64_t)use.r * a.heads + h0 + h] =
+                            sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
+                }
             };
-            __syncthreads();
-#pragma unroll 1
-            for (int h = warp; h < heads; h += W) {
-                // lane w has warp w's
-                const float wm = lane < W ? sm_m[lane % W][h] : -INFINITY, wl = lane < W ? sm_l[lane % W][h] : 0.f;
-                float top = wm;
+            // Maximum and sum over the lanes' parts, and each part's factor.
+            auto over_parts = [&](float2 ml, float &f, float &top, float &sum_l) {
+                top = ml.x;
 #pragma unroll
                 for (int x = 16; x; x >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                const float f = wm == -INFINITY ? 0.f : ex2(wm - top);
-                float sum_l = wl != wl ? wl : wl * f;   // (without a maximum a NaN sum stays one)
+                f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+                sum_l = ml.y != ml.y ? ml.y : ml.y * f;   // (a NaN sum without a maximum stays one)
 #pragma unroll
                 for (int x = 16; x; x >>= 1)
                     sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
+            };
+            auto add = [](float4 &x, float4 y, float w) {
+                x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y);
+                x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+            };
+            constexpr int kQuads = DP > 128 ? 2 : 1;
+            const int c0 = min(4 * lane, DP - 4);   // this lane's columns, and those 128 on
+            const int mine_piece = 2 * (int)blockIdx.x + (ubeg >= begin ? 1 : 0);
+            __syncthreads();
+            // ---- the warps' parts, a head to a warp
+#pragma unroll 1
+            for (int h = warp; h < heads; h += W) {
+                float f, top, sum_l;
+                over_parts(lane < W ? make_float2(sm_m[lane % W][h], sm_l[lane % W][h])
+                                    : make_float2(-INFINITY, 0.f), f, top, sum_l);
                 const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
 #pragma unroll
-                for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
-                    const int c = min(4 * lane + 128 * q, DP - 4);
+                for (int q = 0; q < kQuads; ++q) {
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const float4 y = *reinterpret_cast<const float4 *>(
-                            smem + (w * S::kStages + stage) * S::kStage + at(h, c) * 4);
-                        const float k = __shfl_sync(0xffffffffu, f, w);
-                        x.x = fmaf(y.x, k, x.x), x.y = fmaf(y.y, k, x.y);
-                        x.z = fmaf(y.z, k, x.z), x.w = fmaf(y.w, k, x.w);
-                    }
+                    for (int w = 0; w < W; ++w)
+                        add(x, *reinterpret_cast<const float4 *>(smem + (w * S::kStages + stage) * S::kStage +
+                                                                 at(h, c0 + 128 * q) * 4),
+                            __shfl_sync(0xffffffffu, f, w));
                     if (4 * lane + 128 * q < D)
-                        put(whole, h, c, x, inv);
+                        put(whole, mine_piece, h, 4 * lane + 128 * q, x, inv);
                 }
-                if (lane == 0)
-                    put_sum(whole, h, top, sum_l);
+                put_sum(whole, mine_piece, h, top, sum_l);
             }
             if (!whole) {
                 // A unit's pieces: the second of the block with its first tile,
-                // the first of the others.  kFan of them are joined by their
-                // last block, into the first of them if there are more; those
-                // by their last block.
-                const int c0 = split.block_of(ubeg), c1 = split.block_of(uend - 1);
-                auto piece_of = [&](int b) { return 2 * (int64_t)b + (b == c0 ? 1 : 0); };
-                const int bunches = (c1 - c0) / kFan + 1, b0 = c0 + ((int)blockIdx.x - c0) / kFan * kFan;
-                piece = piece_of(b0);
+                // the first of the others.  kFan of them are joined into the
+                // first of them (into the output if there are no more), then
+                // those; each head by the warp that counts to the last of them.
+                const int b_first = split.block_of(ubeg), b_last = split.block_of(uend - 1);
+                const int bunches = (b_last - b_first) / kFan + 1;
+                const int b0 = b_first + ((int)blockIdx.x - b_first) / kFan * kFan;
+                auto piece_of = [&](int b) { return 2 * b + (b == b_first ? 1 : 0); };
+                const int into = piece_of(b0);
 #pragma unroll 1
-                for (int level = 0; level < 2; ++level) {
-                    const int first = level ? c0 : b0, step = level ? kFan : 1;
-                    const int count = level ? bunches : min(kFan, c1 - b0 + 1);
-                    const bool out = level || bunches == 1;
-                    __syncthreads();   // (the block's writes, ordered by the fence before the count)
-                    if (tid == 0) {
-                        uint32_t *c = level ? ctr + 2 * kMaxCtas + c0 : ctr + piece;
-                        __threadfence();
-                        last = atomicAdd(c, 1u) == (uint32_t)count - 1;
-                        if (last)
-                            *c = 0;
-                        __threadfence();
-                    }
-                    __syncthreads();
-                    if (!last)
-                        break;
+                for (int h = warp; h < heads; h += W) {
 #pragma unroll 1
-                    for (int h = warp; h < heads; h += W) {
-                        // lane i has maximum and sum of pieces i, i + 32, i + 64
-                        float pm[kFan / 32], f[kFan / 32], top = -INFINITY, sum_l = 0.f;
-                        float2 ml[kFan / 32];
-#pragma unroll
-                        for (int k = 0; k < kFan / 32; ++k)
-                            ml[k] = lane + 32 * k < count
-                                        ? __ldcg(reinterpret_cast<const float2 *>(
-                                              pc.at_ml(piece_of(first + (lane + 32 * k) * step), h)))
-                                        : make_float2(-INFINITY, 0.f);
-#pragma unroll
-                        for (int k = 0; k < kFan / 32; ++k)
-                            pm[k] = ml[k].x, top = fmaxf(top, pm[k]);
-#pragma unroll
-                        for (int x = 16; x; x >>= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-#pragma unroll
-                        for (int k = 0; k < kFan / 32; ++k) {
-                            f[k] = pm[k] == -INFINITY ? 0.f : ex2(pm[k] - top);
-                            sum_l += ml[k].y != ml[k].y ? ml[k].y : ml[k].y * f[k];
+                    for (int level = 0; level < 2; ++level) {
+                        const int from = level ? b_first : b0, step = level ? kFan : 1;
+                        const int count = level ? bunches : min(kFan, b_last - b0 + 1);
+                        const bool out = level || bunches == 1;
+                        uint32_t *ctr = reinterpret_cast<uint32_t *>(a.ws) +
+                                        (level ? 2 * kMaxCtas + b_first : into) * kHeads + h;
+                        __syncwarp();
+                        uint32_t done = 0;
+                        if (lane == 0) {
+                            done = count_up(ctr) == (uint32_t)count - 1;
+                            if (done)
+                                *ctr = 0;
                         }
+                        if (!__shfl_sync(0xffffffffu, done, 0))
+                            break;
+                        __syncwarp();   // (what the count has seen, for every lane)
+                        float f, top, sum_l;
+                        float4 y[kQuads][kFan / kQuads], x[kQuads];
+                        auto fill = [&](int i) {
 #pragma unroll
-                        for (int x = 16; x; x >>= 1)
-                            sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
-                        const float inv = !out ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
-#pragma unroll 1
-                        for (int q = 0; q < (DP > 128 ? 2 : 1); ++q) {
-                            const int c = min(4 * lane + 128 * q, DP - 4);
-                            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int z = 0; z < kFan / kQuads; ++z) {
+                                const float *p = pc.at_o(piece_of(from + min(i + z, count - 1) * step), h) + c0;
 #pragma unroll
-                            for (int k = 0; k < kFan / 32; ++k) {
-#pragma unroll 1
-                                for (int i = 0; i < 32 && 32 * k + i < count; i += kBatch) {
-                                    float4 y[kBatch];
-#pragma unroll
-                                    for (int z = 0; z < kBatch; ++z)
-                                        y[z] = 32 * k + i + z < count
-                                                   ? __ldcg(reinterpret_cast<const float4 *>(
-                                                         pc.at_o(piece_of(first + (32 * k + i + z) * step), h) + c))
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                                    for (int z = 0; z < kBatch; ++z) {
-                                        const float w = __shfl_sync(0xffffffffu, f[k], i + z);
-                                        x.x = fmaf(y[z].x, w, x.x), x.y = fmaf(y[z].y, w, x.y);
-                                        x.z = fmaf(y[z].z, w, x.z), x.w = fmaf(y[z].w, w, x.w);
-                                    }
-                                }
+                                for (int q = 0; q < kQuads; ++q)
+                                    y[q][z] = __ldcg(reinterpret_cast<const float4 *>(p + 128 * q));
                             }
-                            if (4 * lane + 128 * q < D)
-                                put(out, h, c, x, inv);
+                        };
+                        fill(0);
+                        over_parts(lane < count ? __ldcg(reinterpret_cast<const float2 *>(
+                                                      pc.at_ml(piece_of(from + lane * step), h)))
+                                                : make_float2(-INFINITY, 0.f), f, top, sum_l);
+#pragma unroll
+                        for (int q = 0; q < kQuads; ++q)
+                            x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                        for (int i = 0;;) {
+#pragma unroll
+                            for (int z = 0; z < kFan / kQuads; ++z) {
+                                const float w = __shfl_sync(0xffffffffu, f, i + z);   // 0 past the last
+#pragma unroll
+                                for (int q = 0; q < kQuads; ++q)
+                                    add(x[q], i + z < count ? y[q][z] : make_float4(0.f, 0.f, 0.f, 0.f), w);
+                            }
+                            i += kFan / kQuads;
+                            if (i >= count)
+                                break;
+                            fill(i);
                         }
-                        if (lane == 0)
-                            put_sum(out, h, top, sum_l);
+                        const float inv = !out ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+#pragma unroll
+                        for (int q = 0; q < kQuads; ++q)
+                            if (4 * lane + 128 * q < D)
+                                put(out, into, h, 4 * lane + 128 * q, x[q], inv);
+                        put_sum(out, into, h, top, sum_l);
+                        if (out)
+                            break;
                     }
-                    if (out)
-                        break;
                 }
             }
             __syncthreads();   // the stages and sums are read
@@ -905,12 +975,19 @@ cudaError_t launch(const PagedAttention &p, uint32_t *err, cudaStream_t stream)
     using S = Shape<DT, DP>;
     static_assert(S::kTile >= kMinTile, "tile bound");
     auto *kernel = k_paged_attention<DT, DP>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     int dev = 0, sms = 0;
-    if (e == cudaSuccess)
-        e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // The kernel's shared memory is asked for once per device, and again
+    // should a launch find it gone (a device that was reset).
+    static std::atomic<uint64_t> asked{0};
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e == cudaSuccess && !(asked.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e == cudaSuccess)
+            asked.fetch_or(bit, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess)
         return e;
     const tw_kv_cache &c = p.cache;
@@ -930,17 +1007,25 @@ cudaError_t launch(const PagedAttention &p, uint32_t *err, cudaStream_t stream)
         if (a.P == 1 << b)
             a.page_shift = b;
     a.cap = (int)key_cap(p.max_pages, c.page_size);
-    a.short_way = a.P % kKeys == 0 && ((a.page_bytes | a.row_bytes | a.head_bytes) >> 32) == 0;
+    a.short_way = a.P % 16 == 0 && ((a.page_bytes | a.row_bytes | a.head_bytes) >> 32) == 0;
     a.mul = p.scale * kLog2e;
     // As many blocks as are resident; no more than tiles that the block table
     // can hold.
     const int64_t tiles = p.requests * a.units * ceil_div(a.cap, S::kTile);
     int64_t grid = (int64_t)sms * S::kBlocks;
     grid = grid < kMaxCtas ? grid : kMaxCtas;
-    static_assert(kFan * kFan >= kMaxCtas, "two joins at most");
+    static_assert(kFan * 32 >= kMaxCtas && S::kWarps <= kFan, "a lane for each part");
     grid = grid < tiles ? grid : tiles;
     kernel<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e == cudaErrorInvalidValue) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e == cudaSuccess) {
+            kernel<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a);
+            e = cudaGetLastError();
+        }
+    }
+    return e;
 }
 
 template <int DT>
@@ -961,11 +1046,11 @@ bool paged_attention_fits(int64_t requests, int64_t heads, int64_t kv_heads, int
                ceil_div(key_cap(max_pages, page_size), kMinTile) <= INT32_MAX;
 }
 
-// Counters (one per piece, one per block), then maxima and sums, then sums of
+// Counters per head (one for each piece, one for each block), then maxima and sums, then sums of
 // values of two pieces per block: the first and the last of its run.
 int64_t paged_attention_ws_bytes(int64_t head_dim)
 {
-    return kMaxCtas * 3 * 4 + (int64_t)kMaxCtas * 2 * kHeads * 4 * (2 + padded(head_dim));
+    return (int64_t)kMaxCtas * kHeads * 4 * (3 + 2 * (2 + padded(head_dim)));
 }
 
 cudaError_t launch_paged_attention(const PagedAttention &a, uint32_t *err, cudaStream_t stream)

@@ -339,10 +339,12 @@ __global__ void __launch_bounds__(kRaThreads) k_rope_append(const RopeAppend a, 
 cudaError_t launch_kv_assign(const KvAssign &a, uint32_t *err, cudaStream_t stream)
 {
     const size_t smem = (size_t)(4 * a.requests + 1) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((4 * kAssignMaxRequests + 1) * sizeof(int32_t)));
-    if (e != cudaSuccess)
-        return e;
+    if (smem > 46 * 1024) {   // (with the static arrays, past the default limit)
+        cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)((4 * kAssignMaxRequests + 1) * sizeof(int32_t)));
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(kAsCtas);
     cfg.blockDim = dim3(kAsThreads);
