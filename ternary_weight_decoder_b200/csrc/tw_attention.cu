@@ -40,12 +40,6 @@
 #ifndef TW_ATT_HALVES
 #define TW_ATT_HALVES 2
 #endif
-#ifndef TW_ATT_RUN
-#define TW_ATT_RUN 2
-#endif
-#ifndef TW_ATT_WHOLE
-#define TW_ATT_WHOLE 4
-#endif
 #ifndef TW_ATT_BLOCKS
 #define TW_ATT_BLOCKS 1
 #endif
@@ -109,7 +103,7 @@ struct Shape {
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kWarps * kStages * (kStage + kScales) + kQueryBytes;
     static_assert(kStages >= 2, "two stages at least");
-    static_assert(kHeads * DP * 4 <= kStage, "a stage holds a warp's sums");
+    static_assert(kFan * DP * 4 <= kStage, "a stage holds a warp's sums, or kFan pieces of one head");
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -347,13 +341,14 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         total += part[w];
     }
     total *= a.units;
-    const uint32_t G = min(gridDim.x, (total + TW_ATT_RUN - 1) / TW_ATT_RUN);   // blocks with tiles
+    const uint32_t G = min(gridDim.x, total);   // blocks with tiles
     const Split split(total, max(G, 1u));
     uint32_t begin = split.begin(min(blockIdx.x, G)), end = split.begin(min(blockIdx.x + 1, G));
+    // A run that would end within `near` tiles of a unit's edge ends there, for
+    // this block and its neighbour alike: a sixth more or less of a run costs
+    // less than another piece.
+    const uint32_t near = split.each / 6;
     if (begin < end) {
-        // Small units are not cut: a run's end inside one moves to the unit's
-        // nearer end, for this block and its neighbour alike.
-        const uint32_t small = max((uint32_t)TW_ATT_WHOLE, split.each / 4);
         const uint32_t mine = before * a.units, past = (before + sum) * a.units;
         if (tid == 0 && end == total)
             bounds[1] = end;
@@ -372,8 +367,8 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             }
             c.u = in / c.s.tiles, c.t = in % c.s.tiles;
             uint32_t to = at;
-            if (c.s.tiles <= small && c.t) {
-                const bool down = 2 * c.t < c.s.tiles;
+            const bool down = 2 * c.t < c.s.tiles;
+            if (c.t && (down ? c.t : c.s.tiles - c.t) <= near) {
                 to = down ? at - c.t : at + c.s.tiles - c.t;
                 c.t = down ? 0 : c.s.tiles - 1;
                 if (!down)
@@ -879,11 +874,12 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 put_sum(whole, mine_piece, h, top, sum_l);
             }
             if (!whole) {
+                __syncthreads();   // every warp's part is read
                 // A unit's pieces: the second of the block with its first tile,
                 // the first of the others.  kFan of them are joined into the
                 // first of them (into the output if there are no more), then
                 // those; each head by the warp that counts to the last of them.
-                const int b_first = split.block_of(ubeg), b_last = split.block_of(uend - 1);
+                const int b_first = split.block_of(ubeg + near), b_last = split.block_of(uend - near - 1);
                 const int bunches = (b_last - b_first) / kFan + 1;
                 const int b0 = b_first + ((int)blockIdx.x - b_first) / kFan * kFan;
                 auto piece_of = [&](int b) { return 2 * b + (b == b_first ? 1 : 0); };
@@ -908,33 +904,39 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                             break;
                         __syncwarp();   // (what the count has seen, for every lane)
                         float f, top, sum_l;
-                        float4 y[kQuads][kFan / kQuads], x[kQuads];
+                        // the pieces come through the warp's stage, every lane
+                        // fetching the columns that it reads
+                        const uint32_t dst = smem_u32(mine) + c0 * 4;
                         auto fill = [&](int i) {
-#pragma unroll
-                            for (int z = 0; z < kFan / kQuads; ++z) {
-                                const float *p = pc.at_o(piece_of(from + min(i + z, count - 1) * step), h) + c0;
+#pragma unroll 4
+                            for (int z = 0; z < kFan; ++z) {
+                                const bool some = i + z < count;
+                                const float *p = pc.at_o(piece_of(from + (some ? i + z : 0) * step), h) + c0;
 #pragma unroll
                                 for (int q = 0; q < kQuads; ++q)
-                                    y[q][z] = __ldcg(reinterpret_cast<const float4 *>(p + 128 * q));
+                                    cp_async16(dst + (z * DP + 128 * q) * 4, p + 128 * q, some);
                             }
+                            commit();
                         };
                         fill(0);
                         over_parts(lane < count ? __ldcg(reinterpret_cast<const float2 *>(
                                                       pc.at_ml(piece_of(from + lane * step), h)))
                                                 : make_float2(-INFINITY, 0.f), f, top, sum_l);
+                        float4 x[kQuads];
 #pragma unroll
                         for (int q = 0; q < kQuads; ++q)
                             x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
                         for (int i = 0;;) {
+                            cp_async_wait<0>();
 #pragma unroll
-                            for (int z = 0; z < kFan / kQuads; ++z) {
+                            for (int z = 0; z < kFan; ++z) {
                                 const float w = __shfl_sync(0xffffffffu, f, i + z);   // 0 past the last
 #pragma unroll
                                 for (int q = 0; q < kQuads; ++q)
-                                    add(x[q], i + z < count ? y[q][z] : make_float4(0.f, 0.f, 0.f, 0.f), w);
+                                    add(x[q], *reinterpret_cast<const float4 *>(mine + z * DP + c0 + 128 * q), w);
                             }
-                            i += kFan / kQuads;
+                            i += kFan;
                             if (i >= count)
                                 break;
                             fill(i);
