@@ -2,33 +2,41 @@
 // tables and slots from request lengths (k_kv_assign), and the rotation of
 // new queries and keys fused with the write of keys and values into their
 // slots (k_rope_append).
+#include <type_traits>
 #include <cooperative_groups.h>
 
 #include "tw_kv.cuh"
 
 namespace cg = cooperative_groups;
 
+
 namespace tw {
 namespace {
 
 // ------------------------------------------------------------- assignment
-constexpr int kAsThreads = 512;
-constexpr int kAsCtas = 8;   // one portable cluster
+constexpr int kAsThreads = 1024;
+constexpr int kAsCtas = 8;          // one portable cluster, or
+constexpr int64_t kAsSmall = 4096;  // a single block up to as many requests and rows
 
-// What one request does in a step.
+__device__ __forceinline__ uint32_t pages_of(int32_t len, uint32_t page)   // len >= 0
+{
+    return ((uint32_t)len + page - 1) / page;
+}
+
+// What one request does in a step (of at most 2^31 - 1 tokens after it).
 struct Step {
-    int64_t now;             // its length after the step
-    int64_t held, need;      // its pages before and after
-    int64_t grown;           // its new tokens
+    int32_t now;             // its length after the step
+    uint32_t held, need;     // its pages before and after
+    int32_t grown;           // its new tokens
 };
 
-__device__ __forceinline__ Step step_of(int32_t len, int32_t delta, int64_t page)
+__device__ __forceinline__ Step step_of(int32_t len, int32_t delta, uint32_t page)
 {
     Step s;
-    s.now = (int64_t)len + delta;
-    s.now = s.now < 0 ? 0 : s.now;
-    s.held = ((int64_t)len + page - 1) / page;
-    s.need = (s.now + page - 1) / page;
+    const int64_t now = (int64_t)len + delta;
+    s.now = (int32_t)min(max(now, (int64_t)0), (int64_t)INT32_MAX);
+    s.held = pages_of(len, page);
+    s.need = pages_of(s.now, page);
     s.grown = s.now > len ? s.now - len : 0;
     return s;
 }
@@ -44,28 +52,29 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane)
     return v;
 }
 
-// One cluster of kAsCtas blocks.  Every block scans all requests for itself
+// One cluster of blocks.  Every block scans all requests for itself
 // (at most kAssignMaxRequests lengths, read from L2), so that the only thing
 // the blocks wait for is that the pages handed back are in the free list
-// before any page is taken from it.  The pages then go out block by block
-// over the requests, and the rows thread by thread: a row finds its request
-// by bisection of the row starts in shared memory, and its page in the block
-// table or, where this step takes it, straight in the free list.
+// before any page is taken from it.  Pages and rows then go out thread by
+// thread: each finds its request by bisection of the prefix sums in shared
+// memory, and a row its page in the block table or, where this step takes it,
+// straight in the free list.
 __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint32_t *err)
 {
     extern __shared__ int32_t sm[];
     const int64_t R = a.requests;
+    const uint32_t page_size = (uint32_t)a.page_size;
     int32_t *start = sm;                 // [R + 1] first row of each request
     int32_t *old = start + R + 1;        // [R]
     int32_t *take = old + R;             // [R] rank of its first page taken
-    int32_t *give = take + R;            // [R] rank of its first page given back
+    int32_t *give = take + R;            // [R + 1] rank of its first page given back
     __shared__ int64_t part[3][kAsThreads / 32];
     __shared__ int64_t total[3];
     __shared__ uint32_t bad;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t gtid = (int64_t)cluster.block_rank() * kAsThreads + tid;
-    const int64_t gthreads = (int64_t)kAsCtas * kAsThreads;
+    const int64_t gthreads = (int64_t)gridDim.x * kAsThreads;
     if (tid == 0)
         bad = 0;
     __syncthreads();
@@ -76,15 +85,15 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
     int64_t sum[3] = {0, 0, 0};
     uint32_t wrong = 0;
     for (int64_t r = lo; r < hi; ++r) {
-        const int32_t len = a.lengths[r];
-        const Step s = step_of(len, a.delta[r], a.page_size);
-        if (len < 0 || s.held > a.max_pages)
+        const int32_t len = max(a.lengths[r], 0), delta = a.delta[r];
+        const Step s = step_of(len, delta, page_size);
+        if (a.lengths[r] < 0 || s.held > a.max_pages)
             wrong |= EFLAG_BADDESC;
-        else if (s.need > a.max_pages || s.now > INT32_MAX)
+        else if (s.need > a.max_pages || (int64_t)len + delta > INT32_MAX)
             wrong |= EFLAG_NOSPACE;
         sum[0] += s.grown;
-        sum[1] += s.need > s.held ? s.need - s.held : 0;
-        sum[2] += s.held > s.need ? s.held - s.need : 0;
+        sum[1] += s.need > s.held ? s.need - s.held : 0u;
+        sum[2] += s.held > s.need ? s.held - s.need : 0u;
     }
     int64_t incl[3];
 #pragma unroll
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
     if (ok)
         for (int64_t r = lo; r < hi; ++r) {
             const int32_t len = a.lengths[r];
-            const Step s = step_of(len, a.delta[r], a.page_size);
+            const Step s = step_of(len, a.delta[r], page_size);
             start[r] = (int32_t)at[0];
             old[r] = len;
             take[r] = (int32_t)at[1];
@@ -131,61 +140,72 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
             at[2] += s.held > s.need ? s.held - s.need : 0;
         }
     if (ok && tid == 0)
-        start[R] = (int32_t)total[0];
+        start[R] = (int32_t)total[0], give[R] = (int32_t)total[2];
     __syncthreads();
 
-    if (ok) {
-        // pages handed back, on top of the list
-        const int64_t gw = (int64_t)cluster.block_rank() * (kAsThreads / 32) + warp;
-        for (int64_t r = gw; r < R; r += kAsCtas * (kAsThreads / 32)) {
-            const Step s = step_of(old[r], a.delta[r], a.page_size);
-            for (int64_t j = s.need + lane; j < s.held; j += 32)
-                a.free_pages[count + give[r] + (j - s.need)] = a.block_table[r * a.table_stride + j];
+    // The last request whose prefix is at or before x: requests that add
+    // nothing share their prefix with the next one.
+    auto owner = [&](const int32_t *prefix, int32_t x) {
+        int l = 0, h = (int)R;
+        while (h - l > 1) {
+            const int m = (l + h) / 2;
+            if (prefix[m] <= x)
+                l = m;
+            else
+                h = m;
         }
+        return l;
+    };
+    // pages handed back, on top of the list
+    const int32_t given = ok ? (int32_t)total[2] : 0, taken = ok ? (int32_t)total[1] : 0;
+    for (int32_t k = (int32_t)gtid; k < given; k += (int32_t)gthreads) {
+        const int r = owner(give, k);
+        // the last of its pages: entry `held` less those that are still to come
+        const int64_t held = pages_of(old[r], page_size);
+        a.free_pages[count + k] = a.block_table[r * a.table_stride + held - (give[r + 1] - k)];
     }
     // Orders the list's new entries, and every read of the inputs that the
     // outputs may overwrite, before what follows in any block.
     cluster.sync();
-    if (ok) {
-        const int64_t gw = (int64_t)cluster.block_rank() * (kAsThreads / 32) + warp;
-        for (int64_t r = gw; r < R; r += kAsCtas * (kAsThreads / 32)) {
-            const Step s = step_of(old[r], a.delta[r], a.page_size);
-            for (int64_t j = s.held + lane; j < s.need; j += 32)
-                a.block_table[r * a.table_stride + j] = a.free_pages[top - 1 - take[r] - (j - s.held)];
-        }
+    for (int32_t k = (int32_t)gtid; k < taken; k += (int32_t)gthreads) {
+        const int r = owner(take, k);
+        const int64_t held = pages_of(old[r], page_size);
+        a.block_table[r * a.table_stride + held + (k - take[r])] = a.free_pages[top - 1 - k];
     }
+    // rows, four in turn to a thread: one bisection, four loads in flight
     const int64_t used = ok ? total[0] : 0;
-    for (int64_t t = gtid; t < a.rows; t += gthreads) {
-        int32_t slot = -1, pos = 0, req = -1;
-        if (t < used) {
-            // the last request whose first row is at or before t (requests
-            // without new rows share their start with the next one)
-            int64_t l = 0, h = R;
-            while (h - l > 1) {
-                const int64_t m = (l + h) / 2;
-                if (start[m] <= t)
-                    l = m;
-                else
-                    h = m;
-            }
-            const int64_t held = ((int64_t)old[l] + a.page_size - 1) / a.page_size;
-            const int64_t p = old[l] + (t - start[l]);
-            const int64_t j = p / a.page_size;
-            const int32_t page = j < held ? a.block_table[l * a.table_stride + j]
-                                          : a.free_pages[top - 1 - take[l] - (j - held)];
-            req = (int32_t)l;
-            pos = (int32_t)p;
-            slot = (int32_t)(page * a.page_size + (p - j * a.page_size));
+    for (int64_t t0 = 4 * gtid; t0 < a.rows; t0 += 4 * gthreads) {
+        int32_t slot[4], pos[4], req[4];
+        int r = t0 < used ? owner(start, (int32_t)t0) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t t = t0 + e;
+            slot[e] = -1, pos[e] = 0, req[e] = -1;
+            if (t >= used)
+                continue;
+            while (start[r + 1] <= t)   // (start[R] = used)
+                ++r;
+            const int32_t p = old[r] + (int32_t)(t - start[r]);
+            const int32_t held = (int32_t)pages_of(old[r], page_size), j = (int32_t)((uint32_t)p / page_size);
+            const int32_t page = j < held ? a.block_table[r * a.table_stride + j]
+                                          : a.free_pages[top - 1 - take[r] - (j - held)];
+            req[e] = r;
+            pos[e] = p;
+            slot[e] = (int32_t)(page * a.page_size + (p - j * a.page_size));
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
-        a.request_of_row[t] = req;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t0 + e < a.rows) {
+                a.slots[t0 + e] = slot[e];
+                a.positions[t0 + e] = pos[e];
+                a.request_of_row[t0 + e] = req[e];
+            }
     }
     // lengths_out may be lengths and free_count_out free_count: every block
     // has its copy of both by now, except of delta, which no output aliases.
     for (int64_t r = gtid; r < R; r += gthreads) {
         if (ok)
-            a.lengths_out[r] = (int32_t)step_of(old[r], a.delta[r], a.page_size).now;
+            a.lengths_out[r] = step_of(old[r], a.delta[r], page_size).now;
         else if (a.lengths_out != a.lengths)
             a.lengths_out[r] = a.lengths[r];
     }
@@ -201,19 +221,35 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
 
 // -------------------------------------------------- rotation and the cache
 constexpr int kRaThreads = 256;
-constexpr int kRaMaxHalf = 128;   // angles of a head of up to 256
+// Warps that a call is split into before a warp takes more heads: 32 on each
+// of 148 SMs (8192 rows of 12 + 2 + 2 heads, 126 MB: one row a warp 24.9 us,
+// half a row 27.5 us, a quarter 31.6 us).
+constexpr int64_t kRaWarps = 4736;
 
-// Angles of far positions: pos * inv_freq is formed in 64 bits and brought
-// into [-pi, pi] there (two pi in two 64-bit parts, each product fused with
-// its sum), and only the reduced angle is rounded to 32 bits, by at most
-// 2^-23: sine and cosine are then as exact as those of a near position.
-__device__ __forceinline__ void angle_sincos(int32_t pos, double freq, float *s, float *c)
+// Sine and cosine of pos * freq.  The angle is formed in 64 bits and brought
+// into [-pi/4, pi/4] there by a whole number k of quarter turns (half a turn
+// in two 64-bit parts, each product fused with its sum; adding 1.5 * 2^52
+// rounds to a whole number and leaves it in the low bits).  What is left, r,
+// is rounded to 32 bits, by at most 2^-25, so that far positions are as exact
+// as near ones; its Taylor series end below 2^-33 (r^11 / 11! and r^12 / 12!
+// at pi/4).  k mod 4 swaps and signs the two.
+__device__ __forceinline__ void angle_sincos(int32_t pos, double freq, float *sin_out, float *cos_out)
 {
-    const double kTwoPiHi = 6.283185307179586232, kTwoPiLo = 2.4492935982947064e-16;
+    const double kQuarterHi = 1.5707963267948966, kQuarterLo = 6.123233995736766e-17;
+    const double kRound = 6755399441055744.0;   // 1.5 * 2^52
     const double a = (double)pos * freq;
-    const double k = rint(a * 0.15915494309189535);
-    const double r = fma(-k, kTwoPiLo, fma(-k, kTwoPiHi, a));
-    sincosf((float)r, s, c);
+    const double sum = fma(a, 0.6366197723675814, kRound);   // 2 / pi
+    const int k = __double2loint(sum);
+    const double n = sum - kRound;
+    const float r = (float)fma(-n, kQuarterLo, fma(-n, kQuarterHi, a)), q = r * r;
+    float s = fmaf(q, 1.0f / 362880, -1.0f / 5040), c = fmaf(q, -1.0f / 3628800, 1.0f / 40320);
+    s = fmaf(q, s, 1.0f / 120), c = fmaf(q, c, -1.0f / 720);
+    s = fmaf(q, s, -1.0f / 6), c = fmaf(q, c, 1.0f / 24);
+    s = fmaf(r * q, s, r), c = fmaf(q, c, -0.5f);
+    c = fmaf(q, c, 1.0f);
+    const float x = k & 1 ? c : s, y = k & 1 ? s : c;
+    *sin_out = k & 2 ? -x : x;
+    *cos_out = (k + 1) & 2 ? -y : y;
 }
 
 template <int DT>
@@ -230,129 +266,199 @@ __device__ __forceinline__ void store4(void *base, int64_t at, float4 v)
     }
 }
 
-// One block per row (token), one warp per head of q, k or v: a lane holds up
-// to two groups of four consecutive columns.  The row's cosines and sines are
-// made once, in shared memory.
-template <int DT>
-__global__ void __launch_bounds__(kRaThreads) k_rope_append(const RopeAppend a, uint32_t *err)
+// A warp takes `per` consecutive heads (of q, then k, then v) of one row: a
+// lane holds QUADS groups of four consecutive columns and makes the cosines
+// and sines that they need once for all of the heads, so nothing is shared
+// and kBatch heads are in flight at a time.  Bound by memory; what has to be
+// kept down is the instructions for a head.
+constexpr int kBatch = 4;
+template <int DT, int QUADS, bool PAIRS>   // PAIRS: (2i, 2i + 1) are turned, else (i, i + rotary / 2)
+__global__ void __launch_bounds__(kRaThreads, QUADS == 1 ? 4 : 2) k_rope_append(const RopeAppend a, int per,
+                                                                                int parts, uint32_t *err)
 {
-    __shared__ __align__(16) float cs[kRaMaxHalf], sn[kRaMaxHalf];
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int half = a.rotary / 2, D = a.head_dim;
-    if (tid < half)
-        angle_sincos(a.positions[t], a.inv_freq[tid], &sn[tid], &cs[tid]);
+    const int lane = threadIdx.x & 31;
+    const uint32_t item = blockIdx.x * (kRaThreads / 32) + (threadIdx.x >> 5);   // below 2^32: the launch sees to it
+    const uint32_t t = item / (uint32_t)parts;
+    if (t >= a.rows)
+        return;
+    const int D = a.head_dim, half = a.rotary / 2;
+    const int first = (int)(item - t * (uint32_t)parts) * per;
     const int64_t slot = a.slots[t];
-    const int64_t slots = a.cache.num_pages * a.cache.page_size;
-    const bool write = slot >= 0 && slot < slots;
-    if (slot >= slots && tid == 0)
+    const bool in_pools = slot < a.cache.num_pages * a.cache.page_size;
+    if (!in_pools && first == 0 && lane == 0)
         atomicOr(err, EFLAG_BADDESC);
-    const int64_t page = write ? slot / a.cache.page_size : 0;
-    const int64_t off = write ? slot - page * a.cache.page_size : 0;
-    __syncthreads();
+    const int pos = a.positions[t];
 
-    const int heads = a.heads + 2 * a.kv_heads;
-    for (int i = warp; i < heads; i += kRaThreads / 32) {
-        const bool is_q = i < a.heads, is_v = i >= a.heads + a.kv_heads;
-        if (!is_q && !write)
-            continue;
-        const int h = is_q ? i : is_v ? i - a.heads - a.kv_heads : i - a.heads;
-        const float *row = is_q   ? a.q + t * a.ldq + (int64_t)h * D
-                           : is_v ? a.v + t * a.ldv + (int64_t)h * D
-                                  : a.k + t * a.ldk + (int64_t)h * D;
-        float4 x[2];
+    // columns 4 * (lane + 32 u) .., and from there to their partners'
+    int col[QUADS], to_other[QUADS];
+    bool in[QUADS], turned[QUADS];
+    float co[QUADS][4], si[QUADS][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int c = 4 * (lane + 32 * u);
-            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c >= D)
+    for (int u = 0; u < QUADS; ++u) {
+        col[u] = 4 * (lane + 32 * u);
+        in[u] = col[u] < D;
+        turned[u] = col[u] < a.rotary;
+        to_other[u] = col[u] < half ? half : -half;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            co[u][e] = 1.f, si[u][e] = 0.f;
+    }
+    auto make_angles = [&] {
+#pragma unroll
+        for (int u = 0; u < QUADS; ++u) {
+            if (!turned[u])
                 continue;
-            x[u] = *reinterpret_cast<const float4 *>(row + c);
-            if (is_v || c >= a.rotary)
-                continue;
-            if (a.interleaved) {
-                const float2 co = *reinterpret_cast<const float2 *>(cs + c / 2);
-                const float2 si = *reinterpret_cast<const float2 *>(sn + c / 2);
-                const float4 y = x[u];
-                x[u] = make_float4(y.x * co.x - y.y * si.x, y.y * co.x + y.x * si.x,
-                                   y.z * co.y - y.w * si.y, y.w * co.y + y.z * si.y);
-            } else {
-                const bool low = c < half;
-                const int p = low ? c : c - half;
-                const float4 y = *reinterpret_cast<const float4 *>(row + (low ? c + half : c - half));
-                const float4 co = *reinterpret_cast<const float4 *>(cs + p);
-                const float4 si = *reinterpret_cast<const float4 *>(sn + p);
-                const float g = low ? -1.f : 1.f;
-                x[u] = make_float4(x[u].x * co.x + g * y.x * si.x, x[u].y * co.y + g * y.y * si.y,
-                                   x[u].z * co.z + g * y.z * si.z, x[u].w * co.w + g * y.w * si.w);
+            const double *f = a.inv_freq + (PAIRS ? col[u] / 2 : col[u] < half ? col[u] : col[u] - half);
+#pragma unroll
+            for (int e = 0; e < (PAIRS ? 2 : 4); ++e) {
+                angle_sincos(pos, f[e], &si[u][e], &co[u][e]);
+                if (!PAIRS && col[u] < half)
+                    si[u][e] = -si[u][e];
             }
         }
-        if (is_q) {
-            // (a warp has read the whole head before it writes: q_out may be q)
+    };
+    // n heads from src on, D columns apart, handed to put(head, u, values);
+    // TURN: rotated.  (Every load of a batch is over before its first store:
+    // q_out may be q.)
+    bool have = false;
+    auto each = [&](auto turn, const float *src, int n, auto put) {
+        constexpr bool TURN = decltype(turn)::value;
+        for (int b = 0; b < n; b += kBatch, src += kBatch * D) {
+            float4 x[kBatch][QUADS], y[kBatch][QUADS];
+            const float *p = src;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k, p += D) {
+                const bool some = b + k < n;
+#pragma unroll
+                for (int u = 0; u < QUADS; ++u) {
+                    x[k][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (some && in[u])
+                        x[k][u] = *reinterpret_cast<const float4 *>(p + col[u]);
+                    if (TURN && !PAIRS) {
+                        y[k][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (some && turned[u])
+                            y[k][u] = *reinterpret_cast<const float4 *>(p + col[u] + to_other[u]);
+                    }
+                }
+            }
+            if (TURN && !have) {   // while the first heads are on their way
+                make_angles();
+                have = true;
+            }
             __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int c = 4 * (lane + 32 * u);
-                if (c < D)
-                    *reinterpret_cast<float4 *>(a.q_out + t * a.ldqo + (int64_t)h * D + c) = x[u];
+            for (int k = 0; k < kBatch; ++k) {
+                if (b + k >= n)
+                    break;
+#pragma unroll
+                for (int u = 0; u < QUADS; ++u) {
+                    const float4 v = x[k][u], w = y[k][u];
+                    if (TURN && PAIRS && turned[u])
+                        x[k][u] = make_float4(v.x * co[u][0] - v.y * si[u][0], v.y * co[u][0] + v.x * si[u][0],
+                                              v.z * co[u][1] - v.w * si[u][1], v.w * co[u][1] + v.z * si[u][1]);
+                    else if (TURN && !PAIRS)
+                        x[k][u] = make_float4(v.x * co[u][0] + w.x * si[u][0], v.y * co[u][1] + w.y * si[u][1],
+                                              v.z * co[u][2] + w.z * si[u][2], v.w * co[u][3] + w.w * si[u][3]);
+                }
+                put(b + k, x[k]);
             }
-            continue;
         }
+    };
+    const int q1 = min(first + per, a.heads);
+    if (first < q1) {
+        float *out = a.q_out + (int64_t)t * a.ldqo + first * D;
+        each(std::true_type{}, a.q + (int64_t)t * a.ldq + first * D, q1 - first, [&](int k, const float4 (&v)[QUADS]) {
+#pragma unroll
+            for (int u = 0; u < QUADS; ++u)
+                if (in[u])
+                    *reinterpret_cast<float4 *>(out + k * D + col[u]) = v[u];
+        });
+    }
+    if (slot < 0 || !in_pools || first + per <= a.heads)
+        return;
+    const uint32_t page = (uint32_t)slot / (uint32_t)a.cache.page_size;
+    const int64_t token = page * a.cache.page_stride +
+                          ((uint32_t)slot - page * (uint32_t)a.cache.page_size) * a.cache.token_stride;
+    auto keep = [&](bool is_v, int h, const float4 (&x)[QUADS]) {
         void *pool = is_v ? a.cache.v : a.cache.k;
-        const int64_t at = page * a.cache.page_stride + off * a.cache.token_stride + h * a.cache.head_stride;
+        const int64_t at = token + h * a.cache.head_stride;
         if constexpr (DT == TW_KV_I8) {
             float m = 0.f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < QUADS; ++u)
                 m = fmaxf(m, fmaxf(fmaxf(fabsf(x[u].x), fabsf(x[u].y)), fmaxf(fabsf(x[u].z), fabsf(x[u].w))));
 #pragma unroll
             for (int o = 16; o; o >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float s = m == 0.f ? 0.f : __fdiv_rn(127.f, m);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int c = 4 * (lane + 32 * u);
-                if (c >= D)
+            for (int u = 0; u < QUADS; ++u) {
+                if (!in[u])
                     continue;
                 const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
                 uint32_t w = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     w |= (uint32_t)(min(max(__float2int_rn(__fmul_rn(v[j], s)), -127), 127) & 0xff) << (8 * j);
-                *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(pool) + at + c) = w;
+                *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(pool) + at + col[u]) = w;
             }
             if (lane == 0)
                 (is_v ? a.cache.v_scale : a.cache.k_scale)[slot * a.kv_heads + h] = __fdiv_rn(m, 127.f);
         } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int c = 4 * (lane + 32 * u);
-                if (c < D)
-                    store4<DT>(pool, at + c, x[u]);
-            }
+            for (int u = 0; u < QUADS; ++u)
+                if (in[u])
+                    store4<DT>(pool, at + col[u], x[u]);
         }
-    }
+    };
+    const int k0 = max(first - a.heads, 0), k1 = min(first + per - a.heads, a.kv_heads);
+    if (k0 < k1)
+        each(std::true_type{}, a.k + (int64_t)t * a.ldk + k0 * D, k1 - k0,
+             [&](int k, const float4 (&v)[QUADS]) { keep(false, k0 + k, v); });
+    const int v0 = max(first - a.heads - a.kv_heads, 0), v1 = min(first + per - a.heads - a.kv_heads, a.kv_heads);
+    if (v0 < v1)
+        each(std::false_type{}, a.v + (int64_t)t * a.ldv + v0 * D, v1 - v0,
+             [&](int k, const float4 (&v)[QUADS]) { keep(true, v0 + k, v); });
+}
+
+template <int DT>
+cudaError_t launch_append(const RopeAppend &a, uint32_t *err, cudaStream_t stream)
+{
+    // Few rows: two heads to a warp, for latency.  Many: a row's heads to as
+    // few warps as leave kRaWarps of them, so that the angles are made less often.
+    const int heads = a.heads + 2 * a.kv_heads;
+    int per = 2;
+    while (per < heads && (a.rows * ceil_div(heads, 2 * per) >= kRaWarps || a.rows * ceil_div(heads, per) > INT32_MAX))
+        per *= 2;
+    const int parts = (int)ceil_div(heads, per);
+    const unsigned grid = (unsigned)ceil_div(a.rows * parts, kRaThreads / 32);
+    auto *kernel = a.head_dim <= 128 ? a.interleaved ? k_rope_append<DT, 1, true> : k_rope_append<DT, 1, false>
+                   : a.interleaved   ? k_rope_append<DT, 2, true>
+                                     : k_rope_append<DT, 2, false>;
+    kernel<<<grid, kRaThreads, 0, stream>>>(a, per, parts, err);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_assign(const KvAssign &a, uint32_t *err, cudaStream_t stream)
 {
-    const size_t smem = (size_t)(4 * a.requests + 1) * sizeof(int32_t);
+    const size_t smem = (size_t)(4 * a.requests + 2) * sizeof(int32_t);
     if (smem > 46 * 1024) {   // (with the static arrays, past the default limit)
         cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)((4 * kAssignMaxRequests + 1) * sizeof(int32_t)));
+                                             (int)((4 * kAssignMaxRequests + 2) * sizeof(int32_t)));
         if (e != cudaSuccess)
             return e;
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kAsCtas);
+    const unsigned ctas = a.requests + a.rows <= kAsSmall ? 1 : kAsCtas;
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kAsThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kAsCtas;
+    at[0].val.clusterDim.x = ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -361,13 +467,11 @@ cudaError_t launch_kv_assign(const KvAssign &a, uint32_t *err, cudaStream_t stre
 
 cudaError_t launch_rope_append(const RopeAppend &a, uint32_t *err, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)a.rows;
     switch ((int)a.cache.dtype) {
-    case TW_KV_BF16: k_rope_append<TW_KV_BF16><<<grid, kRaThreads, 0, stream>>>(a, err); break;
-    case TW_KV_F16: k_rope_append<TW_KV_F16><<<grid, kRaThreads, 0, stream>>>(a, err); break;
-    default: k_rope_append<TW_KV_I8><<<grid, kRaThreads, 0, stream>>>(a, err); break;
+    case TW_KV_BF16: return launch_append<TW_KV_BF16>(a, err, stream);
+    case TW_KV_F16: return launch_append<TW_KV_F16>(a, err, stream);
+    default: return launch_append<TW_KV_I8>(a, err, stream);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace tw

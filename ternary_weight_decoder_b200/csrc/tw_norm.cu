@@ -16,14 +16,10 @@
 namespace tw {
 namespace {
 
-struct NormShape {
-    int threads, per;   // threads a row, groups of V elements a thread
-};
-
-// Sum (or maximum) over the block, in a fixed order: the lanes by butterfly,
-// then the warps' values in order by every thread.
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float *red, int warps)
+// Sum (or maximum) over the threads of a row, in a fixed order: the lanes by
+// butterfly, then (a row of more than one warp) the warps' values in order.
+template <bool MAX, bool WARP>
+__device__ __forceinline__ float row_reduce(float v, float *red, int warps)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -31,7 +27,7 @@ __device__ __forceinline__ float block_reduce(float v, float *red, int warps)
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
         v = MAX ? fmaxf(v, u) : v + u;
     }
-    if (warps == 1)
+    if (WARP)
         return v;
     __syncthreads();   // the last reduction's values are read
     if (lane == 0)
@@ -60,113 +56,117 @@ template <> struct Vec<1> {
     static __device__ __forceinline__ void store(float *p, const float (&v)[1]) { *p = v[0]; }
 };
 
-// Norm of the row held in u[PER][V], in place.
-template <int V, int PER>
-__device__ __forceinline__ void norm_row(float (&u)[PER][V], int kind, const float *w, const float *b,
-                                         int K, float eps, float *red, int threads)
-{
-    const int tid = threadIdx.x, warps = threads / 32;
-    if (kind == TW_NORM_NONE)
-        return;
-    const float inv = 1.0f / (float)K;
-    if (kind == TW_NORM_LAYER) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                s += u[i][j];
-        const float mean = block_reduce<false>(s, red, warps) * inv;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                u[i][j] = (i * threads + tid) * V < K ? u[i][j] - mean : 0.f;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            q = fmaf(u[i][j], u[i][j], q);
-    const float var = block_reduce<false>(q, red, warps) * inv;
-    const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + eps));
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int c = (i * threads + tid) * V;
-        if (c >= K)
-            continue;
-        float wv[V], bv[V];
-        if (w)
-            Vec<V>::load(w + c, wv);
-        if (b)
-            Vec<V>::load(b + c, bv);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            u[i][j] *= r;
-            if (w)
-                u[i][j] *= wv[j];
-            if (b)
-                u[i][j] += bv[j];
-        }
-    }
-}
-
-// One block a row; thread t holds columns V * (t + i * threads).
-template <int V, int PER>
-__global__ void __launch_bounds__(1024) k_residual_norm(const ResidualNorm a)
+// One row by a warp (blocks of kRows rows) or by a block: thread t of the
+// row's `threads` holds columns V * (t + i * threads) + 0 .. V - 1.
+constexpr int kRows = 4;
+template <int V, int PER, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(const ResidualNorm a)
 {
     __shared__ float red[32];
     __shared__ int red_i[32];
-    const int threads = blockDim.x, tid = threadIdx.x, K = (int)a.K;
-    const int64_t m = blockIdx.x;
-    float u[PER][V];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int c = (i * threads + tid) * V;
-        if (c < K) {
-            Vec<V>::load((a.y ? a.y + m * a.ldy : a.x + m * a.ldx) + c, u[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                u[i][j] = 0.f;
-        }
-    }
-    if (a.y) {
-        norm_row<V, PER>(u, a.post, a.post_w, a.post_b, K, a.eps, red, threads);
+    const int threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int K = (int)a.K, warps = threads / 32;
+    const int64_t m = WARP ? (int64_t)blockIdx.x * kRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && m >= a.M)
+        return;
+    const float inv = 1.0f / (float)K;
+    auto col = [&](int i) { return (i * threads + tid) * V; };
+    auto read = [&](const float *row, float (&v)[PER][V]) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int c = (i * threads + tid) * V;
-            if (c >= K)
+            if (col(i) < K) {
+                Vec<V>::load(row + col(i), v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[i][j] = 0.f;
+            }
+        }
+    };
+    auto write = [&](float *row, float (&v)[PER][V]) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (col(i) < K)
+                Vec<V>::store(row + col(i), v[i]);
+    };
+    // Norm of the row in v, in place (columns past K stay 0 until the last step).
+    auto norm = [&](float (&v)[PER][V], int kind, const float *w, const float *b) {
+        if (kind == TW_NORM_NONE)
+            return;
+        if (kind == TW_NORM_LAYER) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    s += v[i][j];
+            const float mean = row_reduce<false, WARP>(s, red, warps) * inv;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[i][j] = col(i) < K ? v[i][j] - mean : 0.f;
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                q = fmaf(v[i][j], v[i][j], q);
+        const float var = row_reduce<false, WARP>(q, red, warps) * inv;
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (col(i) >= K)
                 continue;
-            float g[V], x[V];
-            if (a.gate)
-                Vec<V>::load(a.gate + m * a.ldg + c, g);
-            Vec<V>::load(a.x + m * a.ldx + c, x);
+            float wv[V], bv[V];
+            if (w)
+                Vec<V>::load(w + col(i), wv);
+            if (b)
+                Vec<V>::load(b + col(i), bv);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                u[i][j] = fmaf(a.alpha, a.gate ? u[i][j] * g[j] : u[i][j], x[j]);
+            for (int j = 0; j < V; ++j) {
+                v[i][j] *= r;
+                if (w)
+                    v[i][j] *= wv[j];
+                if (b)
+                    v[i][j] += bv[j];
+            }
         }
-    }
-    if (a.h) {
+    };
+
+    float u[PER][V];
+    if (a.y) {
+        // x is on its way while y is normed, where the registers hold both
+        constexpr bool kAhead = WARP || PER * V <= 16;
+        float x[kAhead ? PER : 1][V];
+        read(a.y + m * a.ldy, u);
+        if constexpr (kAhead)
+            read(a.x + m * a.ldx, x);
+        norm(u, a.post, a.post_w, a.post_b);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int c = (i * threads + tid) * V;
-            if (c < K)
-                Vec<V>::store(a.h + m * a.ldh + c, u[i]);
+            if (col(i) >= K)
+                continue;
+            float g[V];
+            if (a.gate)
+                Vec<V>::load(a.gate + m * a.ldg + col(i), g);
+            if constexpr (!kAhead)
+                Vec<V>::load(a.x + m * a.ldx + col(i), x[0]);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                u[i][j] = fmaf(a.alpha, a.gate ? u[i][j] * g[j] : u[i][j], x[kAhead ? i : 0][j]);
         }
+    } else {
+        read(a.x + m * a.ldx, u);
     }
+    if (a.h)
+        write(a.h + m * a.ldh, u);
     if (!a.n && !a.xq)
         return;
-    norm_row<V, PER>(u, a.pre, a.pre_w, a.pre_b, K, a.eps, red, threads);
-    if (a.n) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = (i * threads + tid) * V;
-            if (c < K)
-                Vec<V>::store(a.n + m * a.ldn + c, u[i]);
-        }
-    }
+    norm(u, a.pre, a.pre_w, a.pre_b);
+    if (a.n)
+        write(a.n + m * a.ldn, u);
     if (!a.xq)
         return;
     float top = 0.f;
@@ -174,14 +174,13 @@ __global__ void __launch_bounds__(1024) k_residual_norm(const ResidualNorm a)
     for (int i = 0; i < PER; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            top = fmaxf(top, (i * threads + tid) * V < K ? fabsf(u[i][j]) : 0.f);
-    top = block_reduce<true>(top, red, threads / 32);
+            top = fmaxf(top, col(i) < K ? fabsf(u[i][j]) : 0.f);
+    top = row_reduce<true, WARP>(top, red, warps);
     const float scale = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int c = (i * threads + tid) * V;
-        if (c >= K)
+        if (col(i) >= K)
             continue;
         uint32_t word = 0;
 #pragma unroll
@@ -191,44 +190,38 @@ __global__ void __launch_bounds__(1024) k_residual_norm(const ResidualNorm a)
             word |= (uint32_t)(q & 0xff) << (8 * j);
         }
         if (V == 4)
-            *reinterpret_cast<uint32_t *>(a.xq + m * a.K + c) = word;
+            *reinterpret_cast<uint32_t *>(a.xq + m * a.K + col(i)) = word;
         else
-            a.xq[m * a.K + c] = (int8_t)word;
+            a.xq[m * a.K + col(i)] = (int8_t)word;
     }
     if (a.qsum) {
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if ((tid & 31) == 0)
-            red_i[tid >> 5] = sum;
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < threads / 32; ++w)
-                sum += red_i[w];
-            a.qsum[m] = sum;
+        if (!WARP) {
+            if ((tid & 31) == 0)
+                red_i[tid >> 5] = sum;
+            __syncthreads();
+            if (tid == 0)
+                for (int w = 1; w < warps; ++w)
+                    sum += red_i[w];
         }
+        if (tid == 0)
+            a.qsum[m] = sum;
     }
     if (tid == 0)
         a.amax[m] = top;
 }
 
-template <int V>
+template <int V, int PER, bool WARP>
 cudaError_t launch(const ResidualNorm &a, cudaStream_t stream)
 {
     const int64_t groups = (a.K + V - 1) / V;
-    // four groups a thread up to 128 threads, then more threads, then more groups
-    int per = 4, threads = 128;
-    while (threads < 1024 && (int64_t)threads * per < groups)
-        threads *= 2;
-    while ((int64_t)threads * per < groups)
-        per *= 2;
-    const unsigned grid = (unsigned)a.M;
-    switch (per) {
-    case 4: k_residual_norm<V, 4><<<grid, threads, 0, stream>>>(a); break;
-    case 8: k_residual_norm<V, 8><<<grid, threads, 0, stream>>>(a); break;
-    case 16: k_residual_norm<V, 16><<<grid, threads, 0, stream>>>(a); break;
-    default: k_residual_norm<V, 32><<<grid, threads, 0, stream>>>(a); break;
-    }
+    if (WARP)
+        k_residual_norm<V, PER, WARP><<<(unsigned)((a.M + kRows - 1) / kRows), 32 * kRows, 0, stream>>>(a);
+    else   // whole warps, PER groups a thread
+        k_residual_norm<V, PER, WARP><<<(unsigned)a.M, (unsigned)((groups + 32 * PER - 1) / (32 * PER) * 32), 0,
+                                        stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -244,7 +237,17 @@ cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
                        a.ldh % 4 == 0 && a.ldn % 4 == 0 && by16(a.x) && by16(a.y) && by16(a.gate) &&
                        by16(a.post_w) && by16(a.post_b) && by16(a.pre_w) && by16(a.pre_b) &&
                        by16(a.h) && by16(a.n) && by16(a.xq);
-    return quads ? launch<4>(a, stream) : launch<1>(a, stream);
+    if (!quads) {
+        if (a.K <= 4096)
+            return launch<1, 4, false>(a, stream);
+        return a.K <= 8192 ? launch<1, 8, false>(a, stream) : launch<1, 32, false>(a, stream);
+    }
+    const int64_t groups = a.K / 4;
+    if (groups <= 512 && a.M < 148)
+        return launch<4, 1, false>(a, stream);
+    if (groups <= 1024)
+        return launch<4, 2, false>(a, stream);
+    return groups <= 4096 ? launch<4, 4, false>(a, stream) : launch<4, 8, false>(a, stream);
 }
 
 }  // namespace tw
