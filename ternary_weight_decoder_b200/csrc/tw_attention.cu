@@ -32,16 +32,22 @@
 #include "tw_kv.cuh"
 
 #ifndef TW_ATT_WARPS
-#define TW_ATT_WARPS 8
+#define TW_ATT_WARPS 6
 #endif
 #ifndef TW_ATT_WARPS_CODES
-#define TW_ATT_WARPS_CODES 12
+#define TW_ATT_WARPS_CODES 6
 #endif
 #ifndef TW_ATT_HALVES
 #define TW_ATT_HALVES 2
 #endif
+#ifndef TW_ATT_WARPS_WIDE
+#define TW_ATT_WARPS_WIDE 6
+#endif
+#ifndef TW_ATT_BLOCKS_WIDE
+#define TW_ATT_BLOCKS_WIDE 1
+#endif
 #ifndef TW_ATT_BLOCKS
-#define TW_ATT_BLOCKS 1
+#define TW_ATT_BLOCKS 2
 #endif
 
 namespace tw {
@@ -93,12 +99,12 @@ struct Shape {
     static constexpr int kSteps = DP / 16;             // 16 columns of values each
     static constexpr int kQueryParts = kBf || kCodes ? 3 : 2;
     static constexpr int kQuerySteps = kCodes ? DP / 32 : DP / 16;   // MMA steps over a key
-    static constexpr int kWarps = (kCodes ? TW_ATT_WARPS_CODES : TW_ATT_WARPS) / (DP > 128 ? 2 : 1);
+    static constexpr int kWarps = DP > 128 ? TW_ATT_WARPS_WIDE : kCodes ? TW_ATT_WARPS_CODES : TW_ATT_WARPS;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kKeys * kWarps;
-    static constexpr int kBlocks = TW_ATT_BLOCKS;      // resident on an SM
+    static constexpr int kBlocks = DP > 128 ? TW_ATT_BLOCKS_WIDE : TW_ATT_BLOCKS;   // resident on an SM
     static constexpr int kQueryBytes = kQuerySteps * kQueryParts * 32 * 8;   // a unit's queries, as operands
-    static constexpr int kRoom = (227 * 1024) / kBlocks - 5120 - kQueryBytes;
+    static constexpr int kRoom = (227 * 1024) / kBlocks - 3072 - kQueryBytes;
     static constexpr int kFit = kRoom / (kWarps * (kStage + kScales));
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kWarps * kStages * (kStage + kScales) + kQueryBytes;
