@@ -61,6 +61,10 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 // A call, as the kernel reads it.
 struct Args {
+    // KV head and first of its query heads of a unit
+    __device__ __forceinline__ int kv_of(int u) const { return per_kv == 1 ? u : u / per_kv; }
+    __device__ __forceinline__ int skip_of(int u, int kv) const { return (u - kv * per_kv) * kHeads; }
+
     const float *q;
     float *out, *lse;
     const int32_t *table, *lengths, *first;
@@ -356,10 +360,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     const uint32_t near = split.each / 6;
     if (begin < end) {
         const uint32_t mine = before * a.units, past = (before + sum) * a.units;
-        if (tid == 0 && end == total)
+        if (tid == 0 && (near == 0 || end == total))
             bounds[1] = end;
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < (near ? 2 : 1); ++k) {
             const uint32_t at = k ? end : begin;
             if (at < mine || at >= past)
                 continue;
@@ -410,12 +414,20 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     const uint8_t *kpool;
     int head;
     auto enter_unit = [&] {
-        head = load.u / a.per_kv;
+        head = a.kv_of(load.u);
         table = a.table + load.r * a.table_stride;
         kpool = a.k + head * a.head_bytes + row0 * a.row_bytes + chunk * 16;
+        // its queries are on their way to L1 while its keys are fetched
+        const int skip = a.skip_of(load.u, head);
+        const float *row = a.q + load.r * a.ldq + (int64_t)(head * a.group + skip + warp) * D;
+        float x, y, z, w;
+        if (warp < min(kHeads, a.group - skip) && 4 * lane < D)
+            asm volatile("ld.global.ca.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "l"(row + 4 * lane));
     };
-    // The next step's first key and, for every 16 keys that are visible and
-    // share a page (the short way), that page: looked up a step early.
+    // The next step's first key and, for every 16 keys of which some are
+    // visible, their page (the short way: pages hold whole sixteens of keys),
+    // looked up a step early.
     int next_j = 0, next_in[H] = {}, next_page[H];
     auto look_up = [&] {
         next_j = (load.s.first_tile + load.t) * kTile + warp * S::kKeys;
@@ -423,7 +435,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         for (int h = 0; h < H; ++h) {
             const int j = next_j + 16 * h;
             next_page[h] = -1;
-            if (a.short_way && j >= load.s.lo && j + 16 <= load.s.hi) {
+            if (a.short_way && j < load.s.hi && j + 16 > load.s.lo) {
                 const int p = a.page_shift >= 0 ? j >> a.page_shift : j / a.P;
                 next_in[h] = j - p * a.P;
                 next_page[h] = __ldg(table + p);
@@ -437,14 +449,23 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         int64_t slot = -1;   // codes: this lane's key
         auto half = [&](int h, int page0, int in0) {
             const uint32_t rows = base + h * 16 * S::kRow;
-            if ((uint32_t)page0 < (uint32_t)a.pages) {
+            if (a.short_way) {
+                // visible keys of the sixteen, from which to which
+                const int from = max(load.s.lo - next_j - 16 * h, 0), to = min(load.s.hi - next_j - 16 * h, 16);
+                if (from >= to)
+                    return;   // none: a whole step of these is passed over, half a one is masked below
+                if ((uint32_t)page0 >= (uint32_t)a.pages) {
+                    if (lane == 0)
+                        atomicOr(a.err, EFLAG_BADDESC);
+                    return;
+                }
                 const uint8_t *ks = kpool + (uint64_t)(uint32_t)page0 * (uint32_t)a.page_bytes +
                                     (uint64_t)(uint32_t)in0 * (uint32_t)a.row_bytes;
                 const uint8_t *vs = ks + a.v_of_k;
-                mask |= 0xffffu << (16 * h);
-                if (S::kCodes && (lane >> 4) == h)
+                if (S::kCodes && (lane >> 4) == h && (lane & 15) >= from && (lane & 15) < to)
                     slot = (uint32_t)(page0 * a.P + in0) + (lane & 15);
-                if (kWide || in_row) {
+                if (to - from == 16 && (kWide || in_row)) {
+                    mask |= 0xffffu << (16 * h);
 #pragma unroll
                     for (int i = 0; i < 16 / kRowsPer; ++i) {
                         const uint32_t dst = (lane_dst + rows) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
@@ -453,12 +474,16 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                                    !kWide || in_row);
                         ks += kRowsPer * a.row_bytes, vs += kRowsPer * a.row_bytes;
                     }
-                } else {   // past head_dim: zeros
+                } else {   // zeros for keys that are not visible and columns past head_dim
+                    mask |= (0xffffu >> (16 - to + from)) << (16 * h + from);
 #pragma unroll 1
                     for (int i = 0; i < 16 / kRowsPer; ++i) {
                         const uint32_t dst = (lane_dst + rows) ^ (row_swap<S::kChunks>(kRowsPer * i) << 4);
-                        cp_async16(dst + kRowsPer * i * S::kRow, a.k, false);
-                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, a.k, false);
+                        const int row = row0 + kRowsPer * i;
+                        const bool in = in_row && row >= from && row < to;
+                        cp_async16(dst + kRowsPer * i * S::kRow, in ? ks : a.k, in);
+                        cp_async16(dst + kRowsPer * i * S::kRow + S::kPool, in ? vs : a.k, in);
+                        ks += kRowsPer * a.row_bytes, vs += kRowsPer * a.row_bytes;
                     }
                 }
                 return;
@@ -540,8 +565,8 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
 
         // ---- a new piece: its queries, a head to a warp, split
         if (fresh) {
-            const int h0 = (use.u / a.per_kv) * a.group + (use.u % a.per_kv) * kHeads;
-            const int heads = min(kHeads, a.group - (use.u % a.per_kv) * kHeads);
+            const int kv = a.kv_of(use.u), skip = a.skip_of(use.u, kv);
+            const int h0 = kv * a.group + skip, heads = min(kHeads, a.group - skip);
 #pragma unroll 1
             for (int h = warp; h < kHeads; h += W) {
                 const float *row = a.q + use.r * a.ldq + (int64_t)(h0 + h) * D;
@@ -797,8 +822,8 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         const bool unit_done = use.t + 1 == use.s.tiles;
         if (unit_done || i + 1 == n) {
             const uint32_t ubeg = begin + i - use.t, uend = ubeg + use.s.tiles;
-            const int h0 = (use.u / a.per_kv) * a.group + (use.u % a.per_kv) * kHeads;
-            const int heads = min(kHeads, a.group - (use.u % a.per_kv) * kHeads);
+            const int kv = a.kv_of(use.u), skip = a.skip_of(use.u, kv);
+            const int h0 = kv * a.group + skip, heads = min(kHeads, a.group - skip);
             __syncwarp();   // the stage is read: it takes the warp's sums
             float *mine = reinterpret_cast<float *>(smem + (warp * S::kStages + stage) * S::kStage);
             // [head][column], columns permuted by the head against bank conflicts
