@@ -15,8 +15,9 @@
 // are.  A block whose run holds all of a (request, KV head) writes its
 // output; the pieces of one that spans blocks go to the workspace and are
 // joined in a fixed order, each head by the warp that finishes it last, kFan
-// pieces at a time and then those.  Inside a block each warp takes 16 keys of every tile
-// through its own ring of cp.async stages: no barrier until a piece ends.
+// pieces at a time and then those.  Inside a block each warp takes 16 keys (32
+// of codes) of every tile through its own ring of cp.async stages: no barrier
+// until a piece ends.
 //
 // Matrix products: the 16 keys (or 16 columns of the values) are the rows of
 // an MMA, eight query heads its columns, so no lane computes for nobody:
@@ -24,31 +25,18 @@
 // are carried in parts, each the rounding of what the last one left: two of
 // fp16 (22 bits), three of bf16 (24 bits); queries on codes in three int8
 // digits (23 bits of the head's largest), whose products are exact integers.
-// Scores and sums are fp32.
-// Groups of more than eight heads are split into units of eight.
+// Scores and sums are fp32.  Groups of more than eight heads are split into
+// units of eight, which read their keys again (from L2, mostly).
+//
+// Measured on B200 (12 heads over 2 KV heads of 128): past the first 262144
+// keys of one request, another 262144 take 36.9 us of bf16 (7.3 TB/s) and
+// 21.2 us of codes (6.7 TB/s), the memory's rate; what is left is the start
+// (scanning lengths, looking up pages, the first keys: about 5 us) and the
+// joins (2 to 6 us).
 #include <atomic>
 #include <cfloat>
 
 #include "tw_kv.cuh"
-
-#ifndef TW_ATT_WARPS
-#define TW_ATT_WARPS 6
-#endif
-#ifndef TW_ATT_WARPS_CODES
-#define TW_ATT_WARPS_CODES 6
-#endif
-#ifndef TW_ATT_HALVES
-#define TW_ATT_HALVES 2
-#endif
-#ifndef TW_ATT_WARPS_WIDE
-#define TW_ATT_WARPS_WIDE 6
-#endif
-#ifndef TW_ATT_BLOCKS_WIDE
-#define TW_ATT_BLOCKS_WIDE 1
-#endif
-#ifndef TW_ATT_BLOCKS
-#define TW_ATT_BLOCKS 2
-#endif
 
 namespace tw {
 namespace {
@@ -56,7 +44,7 @@ namespace {
 constexpr int kMaxCtas = 512;                // counters and partial results in the workspace
 constexpr int kHeads = 8;                    // query heads of a unit
 constexpr int kFan = 16;                     // pieces that one warp joins, of one head
-constexpr int kMinTile = 32;                 // keys of the smallest variant's tile
+constexpr int kMinTile = 96;                 // keys of the smallest variant's tile
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 // A call, as the kernel reads it.
@@ -94,7 +82,7 @@ struct Shape {
     static constexpr int kChunks = kRow / 16;
     // Keys of a warp's step: twice 16 of codes, so that a step moves as many
     // bytes and its fixed instructions count for as little as of 16 bits.
-    static constexpr int kHalves = kCodes ? TW_ATT_HALVES : 1;
+    static constexpr int kHalves = kCodes ? 2 : 1;
     static constexpr int kKeys = 16 * kHalves;
     static constexpr uint32_t kAll = kHalves == 2 ? 0xffffffffu : 0xffffu;
     static constexpr int kPool = kKeys * kRow;         // bytes of a step's keys
@@ -103,10 +91,15 @@ struct Shape {
     static constexpr int kSteps = DP / 16;             // 16 columns of values each
     static constexpr int kQueryParts = kBf || kCodes ? 3 : 2;
     static constexpr int kQuerySteps = kCodes ? DP / 32 : DP / 16;   // MMA steps over a key
-    static constexpr int kWarps = DP > 128 ? TW_ATT_WARPS_WIDE : kCodes ? TW_ATT_WARPS_CODES : TW_ATT_WARPS;
+    // Two blocks of six warps on an SM: while one ends a piece (a few thousand
+    // cycles of latencies) the other streams.  256 requests of 512 .. 16384
+    // keys of codes: 129 us, against 143 us with one block of twelve; 512 of
+    // 20 .. 300 bf16 keys: 30.7 / 41.2 us; one of 131072: 34.3 / 36.7 us.
+    // Rows of more than 128 columns take a whole SM's shared memory.
+    static constexpr int kWarps = 6;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kKeys * kWarps;
-    static constexpr int kBlocks = DP > 128 ? TW_ATT_BLOCKS_WIDE : TW_ATT_BLOCKS;   // resident on an SM
+    static constexpr int kBlocks = DP > 128 ? 1 : 2;   // resident on an SM
     static constexpr int kQueryBytes = kQuerySteps * kQueryParts * 32 * 8;   // a unit's queries, as operands
     static constexpr int kRoom = (227 * 1024) / kBlocks - 3072 - kQueryBytes;
     static constexpr int kFit = kRoom / (kWarps * (kStage + kScales));
@@ -224,14 +217,20 @@ struct Span {
 };
 
 template <int TILE>
-__device__ __forceinline__ Span span_of(const Args &a, int r)
+__device__ __forceinline__ Span span_of(const Args &a, int length, int first)
 {
     Span s;
-    s.hi = min(a.lengths[r], a.cap);
-    s.lo = a.first ? max(a.first[r], 0) : 0;
+    s.hi = min(length, a.cap);
+    s.lo = max(first, 0);
     s.first_tile = s.lo / TILE;
     s.tiles = s.hi > s.lo ? (s.hi - 1) / TILE + 1 - s.first_tile : 0;
     return s;
+}
+
+template <int TILE>
+__device__ __forceinline__ Span span_of(const Args &a, int r)
+{
+    return span_of<TILE>(a, a.lengths[r], a.first ? a.first[r] : 0);
 }
 
 // A place in the run of tiles: tile t of unit u of request r.
@@ -239,6 +238,14 @@ template <int TILE>
 struct Cursor {
     int r, u, t;
     Span s;
+    int length, first;   // of request r + 1, read on entering r
+    __device__ __forceinline__ void ahead(const Args &a)
+    {
+        if (r + 1 < a.requests) {
+            length = a.lengths[r + 1];
+            first = a.first ? a.first[r + 1] : 0;
+        }
+    }
     // One tile on; whether that is another unit.
     __device__ __forceinline__ bool next(const Args &a)
     {
@@ -251,7 +258,8 @@ struct Cursor {
         do {
             if (++r >= a.requests)
                 return true;
-            s = span_of<TILE>(a, r);
+            s = span_of<TILE>(a, length, first);
+            ahead(a);
         } while (s.tiles == 0);
         return true;
     }
@@ -381,8 +389,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             if (c.t && (down ? c.t : c.s.tiles - c.t) <= near) {
                 to = down ? at - c.t : at + c.s.tiles - c.t;
                 c.t = down ? 0 : c.s.tiles - 1;
-                if (!down)
+                if (!down) {
+                    c.ahead(a);
                     c.next(a);
+                }
             }
             bounds[k] = to;
             if (k == 0)
@@ -399,6 +409,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     Cursor<kTile> load, use;
     load.r = start[0], load.u = start[1], load.t = start[2];
     load.s = span_of<kTile>(a, load.r);
+    load.ahead(a);
     use = load;
 
     // ---- the ring of stages
@@ -533,6 +544,48 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+    // ---- sums of a unit, whole or in pieces
+    struct Unit {
+        int r, h0, heads;         // request, first query head, heads (0: none)
+        uint32_t beg, end;        // its tiles
+    };
+    Unit before_it{}, after{};    // this block's pieces: of a unit that began before its run, or ends after it
+    Pieces<DP> pc;
+    pc.ml = reinterpret_cast<float *>(a.ws) + 3 * kMaxCtas * kHeads;
+    pc.o = pc.ml + kMaxCtas * 2 * 2 * kHeads;
+    // Column c of head h into the output, or into a piece.
+    auto put = [&](const Unit &u, bool out, int piece, int h, int c, float4 x, float inv) {
+        float *to = out ? a.out + u.r * a.ldo + (int64_t)(u.h0 + h) * D : pc.at_o(piece, h);
+        *reinterpret_cast<float4 *>(to + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    };
+    auto put_sum = [&](const Unit &u, bool out, int piece, int h, float top, float sum_l) {
+        if (lane == 0) {
+            if (!out)
+                *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
+            else if (a.lse)
+                a.lse[(int64_t)u.r * a.heads + u.h0 + h] =
+                    sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
+        }
+    };
+    // Maximum and sum over the lanes' parts, and each part's factor.
+    auto over_parts = [&](float2 ml, float &f, float &top, float &sum_l) {
+        top = ml.x;
+#pragma unroll
+        for (int x = 16; x; x >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+        sum_l = ml.y != ml.y ? ml.y : ml.y * f;   // (a NaN sum without a maximum stays one)
+#pragma unroll
+        for (int x = 16; x; x >>= 1)
+            sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
+    };
+    auto add = [](float4 &x, float4 y, float w) {
+        x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y);
+        x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+    };
+    constexpr int kQuads = DP > 128 ? 2 : 1;
+    const int c0 = min(4 * lane, DP - 4);   // this lane's columns, and those 128 on
 
     // Queries as the MMA's B operand, in parts: [step][part][lane] the two
     // words that a lane feeds for head lane / 4 of the unit.
@@ -847,42 +900,8 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 }
             }
             const bool whole = unit_done && ubeg >= begin;
-            Pieces<DP> pc;
-            pc.ml = reinterpret_cast<float *>(a.ws) + 3 * kMaxCtas * kHeads;
-            pc.o = pc.ml + kMaxCtas * 2 * 2 * kHeads;
-            // Column c of head h into the output, or into a piece.
-            auto put = [&](bool out, int piece, int h, int c, float4 x, float inv) {
-                float *to = out ? a.out + use.r * a.ldo + (int64_t)(h0 + h) * D : pc.at_o(piece, h);
-                *reinterpret_cast<float4 *>(to + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-            };
-            auto put_sum = [&](bool out, int piece, int h, float top, float sum_l) {
-                if (lane == 0) {
-                    if (!out)
-                        *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
-                    else if (a.lse)
-                        a.lse[(int64_t)use.r * a.heads + h0 + h] =
-                            sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
-                }
-            };
-            // Maximum and sum over the lanes' parts, and each part's factor.
-            auto over_parts = [&](float2 ml, float &f, float &top, float &sum_l) {
-                top = ml.x;
-#pragma unroll
-                for (int x = 16; x; x >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-                sum_l = ml.y != ml.y ? ml.y : ml.y * f;   // (a NaN sum without a maximum stays one)
-#pragma unroll
-                for (int x = 16; x; x >>= 1)
-                    sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
-            };
-            auto add = [](float4 &x, float4 y, float w) {
-                x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y);
-                x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
-            };
-            constexpr int kQuads = DP > 128 ? 2 : 1;
-            const int c0 = min(4 * lane, DP - 4);   // this lane's columns, and those 128 on
             const int mine_piece = 2 * (int)blockIdx.x + (ubeg >= begin ? 1 : 0);
+            const Unit unit{use.r, h0, heads, ubeg, uend};
             __syncthreads();
             // ---- the warps' parts, a head to a warp
 #pragma unroll 1
@@ -900,89 +919,12 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                                                                  at(h, c0 + 128 * q) * 4),
                             __shfl_sync(0xffffffffu, f, w));
                     if (4 * lane + 128 * q < D)
-                        put(whole, mine_piece, h, 4 * lane + 128 * q, x, inv);
+                        put(unit, whole, mine_piece, h, 4 * lane + 128 * q, x, inv);
                 }
-                put_sum(whole, mine_piece, h, top, sum_l);
+                put_sum(unit, whole, mine_piece, h, top, sum_l);
             }
-            if (!whole) {
-                __syncthreads();   // every warp's part is read
-                // A unit's pieces: the second of the block with its first tile,
-                // the first of the others.  kFan of them are joined into the
-                // first of them (into the output if there are no more), then
-                // those; each head by the warp that counts to the last of them.
-                const int b_first = split.block_of(ubeg + near), b_last = split.block_of(uend - near - 1);
-                const int bunches = (b_last - b_first) / kFan + 1;
-                const int b0 = b_first + ((int)blockIdx.x - b_first) / kFan * kFan;
-                auto piece_of = [&](int b) { return 2 * b + (b == b_first ? 1 : 0); };
-                const int into = piece_of(b0);
-#pragma unroll 1
-                for (int h = warp; h < heads; h += W) {
-#pragma unroll 1
-                    for (int level = 0; level < 2; ++level) {
-                        const int from = level ? b_first : b0, step = level ? kFan : 1;
-                        const int count = level ? bunches : min(kFan, b_last - b0 + 1);
-                        const bool out = level || bunches == 1;
-                        uint32_t *ctr = reinterpret_cast<uint32_t *>(a.ws) +
-                                        (level ? 2 * kMaxCtas + b_first : into) * kHeads + h;
-                        __syncwarp();
-                        uint32_t done = 0;
-                        if (lane == 0) {
-                            done = count_up(ctr) == (uint32_t)count - 1;
-                            if (done)
-                                *ctr = 0;
-                        }
-                        if (!__shfl_sync(0xffffffffu, done, 0))
-                            break;
-                        __syncwarp();   // (what the count has seen, for every lane)
-                        float f, top, sum_l;
-                        // the pieces come through the warp's stage, every lane
-                        // fetching the columns that it reads
-                        const uint32_t dst = smem_u32(mine) + c0 * 4;
-                        auto fill = [&](int i) {
-#pragma unroll 4
-                            for (int z = 0; z < kFan; ++z) {
-                                const bool some = i + z < count;
-                                const float *p = pc.at_o(piece_of(from + (some ? i + z : 0) * step), h) + c0;
-#pragma unroll
-                                for (int q = 0; q < kQuads; ++q)
-                                    cp_async16(dst + (z * DP + 128 * q) * 4, p + 128 * q, some);
-                            }
-                            commit();
-                        };
-                        fill(0);
-                        over_parts(lane < count ? __ldcg(reinterpret_cast<const float2 *>(
-                                                      pc.at_ml(piece_of(from + lane * step), h)))
-                                                : make_float2(-INFINITY, 0.f), f, top, sum_l);
-                        float4 x[kQuads];
-#pragma unroll
-                        for (int q = 0; q < kQuads; ++q)
-                            x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-                        for (int i = 0;;) {
-                            cp_async_wait<0>();
-#pragma unroll
-                            for (int z = 0; z < kFan; ++z) {
-                                const float w = __shfl_sync(0xffffffffu, f, i + z);   // 0 past the last
-#pragma unroll
-                                for (int q = 0; q < kQuads; ++q)
-                                    add(x[q], *reinterpret_cast<const float4 *>(mine + z * DP + c0 + 128 * q), w);
-                            }
-                            i += kFan;
-                            if (i >= count)
-                                break;
-                            fill(i);
-                        }
-                        const float inv = !out ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
-#pragma unroll
-                        for (int q = 0; q < kQuads; ++q)
-                            if (4 * lane + 128 * q < D)
-                                put(out, into, h, 4 * lane + 128 * q, x[q], inv);
-                        put_sum(out, into, h, top, sum_l);
-                        if (out)
-                            break;
-                    }
-                }
-            }
+            if (!whole)   // joined when the run is over: nothing in it waits for the counts
+                (ubeg >= begin ? after : before_it) = unit;
             __syncthreads();   // the stages and sums are read
             fresh = true;
         }
@@ -990,6 +932,110 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
+    __syncwarp();   // the warp's stages are its own again
+    float *mine = reinterpret_cast<float *>(smem + warp * S::kStages * S::kStage);
+    // A unit's pieces: the second of the block with its first tile, the first
+    // of the others.  kFan of them are joined into the first of them (into the
+    // output if there are no more), then those; each head by the warp that
+    // counts to the last of them.
+    struct Join {
+        int b_first, b_last, b0, into, bunches;
+    };
+    auto piece_of = [](const Join &j, int b) { return 2 * b + (b == j.b_first ? 1 : 0); };
+    auto join_of = [&](const Unit &u) {
+        Join j;
+        j.b_first = split.block_of(u.beg + near), j.b_last = split.block_of(u.end - near - 1);
+        j.bunches = (j.b_last - j.b_first) / kFan + 1;
+        j.b0 = j.b_first + ((int)blockIdx.x - j.b_first) / kFan * kFan;
+        j.into = piece_of(j, j.b0);
+        return j;
+    };
+    auto in_bunch = [&](const Join &j) { return min(kFan, j.b_last - j.b0 + 1); };
+    const Join join_0 = before_it.heads ? join_of(before_it) : Join{}, join_1 = after.heads ? join_of(after) : Join{};
+    uint32_t *counters = reinterpret_cast<uint32_t *>(a.ws);
+    auto last_of = [&](uint32_t *ctr, int count) {
+        const bool is = count_up(ctr) == (uint32_t)count - 1;
+        if (is)
+            *ctr = 0;
+        return is;
+    };
+#pragma unroll 1
+    for (int h = warp; h < max(before_it.heads, after.heads); h += W) {
+        // lane 0 counts for the first piece, lane 1 for the second, at once
+        bool done = false;
+        if (lane < 2 && h < (lane ? after.heads : before_it.heads))
+            done = last_of(counters + (lane ? join_1.into : join_0.into) * kHeads + h,
+                           in_bunch(lane ? join_1 : join_0));
+        const uint32_t whose = __ballot_sync(0xffffffffu, done);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            if (!((whose >> k) & 1))
+                continue;
+            const Unit unit = k ? after : before_it;
+            const Join j = k ? join_1 : join_0;
+#pragma unroll 1
+            for (int level = 0; level < 2; ++level) {
+                const int from = level ? j.b_first : j.b0, step = level ? kFan : 1;
+                const int count = level ? j.bunches : in_bunch(j);
+                const bool out = level || j.bunches == 1;
+                if (level) {
+                    __syncwarp();
+                    bool last = false;
+                    if (lane == 0)
+                        last = last_of(counters + (2 * kMaxCtas + j.b_first) * kHeads + h, count);
+                    if (!__shfl_sync(0xffffffffu, last, 0))
+                        break;
+                }
+                __syncwarp();   // (what the count has seen, for every lane)
+                float f, top, sum_l;
+                // the pieces come through the warp's stage, every lane
+                // fetching the columns that it reads
+                const uint32_t dst = smem_u32(mine) + c0 * 4;
+                auto fill = [&](int i) {
+#pragma unroll 4
+                    for (int z = 0; z < kFan; ++z) {
+                        const bool some = i + z < count;
+                        const float *p = pc.at_o(piece_of(j, from + (some ? i + z : 0) * step), h) + c0;
+#pragma unroll
+                        for (int q = 0; q < kQuads; ++q)
+                            cp_async16(dst + (z * DP + 128 * q) * 4, p + 128 * q, some);
+                    }
+                    commit();
+                };
+                fill(0);
+                over_parts(lane < count ? __ldcg(reinterpret_cast<const float2 *>(
+                                              pc.at_ml(piece_of(j, from + lane * step), h)))
+                                        : make_float2(-INFINITY, 0.f), f, top, sum_l);
+                float4 x[kQuads];
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q)
+                    x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int i = 0;;) {
+                    cp_async_wait<0>();
+#pragma unroll
+                    for (int z = 0; z < kFan; ++z) {
+                        const float w = __shfl_sync(0xffffffffu, f, i + z);   // 0 past the last
+#pragma unroll
+                        for (int q = 0; q < kQuads; ++q)
+                            add(x[q], *reinterpret_cast<const float4 *>(mine + z * DP + c0 + 128 * q), w);
+                    }
+                    i += kFan;
+                    if (i >= count)
+                        break;
+                    fill(i);
+                }
+                const float inv = !out ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q)
+                    if (4 * lane + 128 * q < D)
+                        put(unit, out, j.into, h, 4 * lane + 128 * q, x[q], inv);
+                put_sum(unit, out, j.into, h, top, sum_l);
+                if (out)
+                    break;
+            }
+        }
+    }
     clear_rows();
 }
 
