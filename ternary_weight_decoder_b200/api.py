@@ -22,6 +22,12 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python -m ternary_weight_decoder_b200.build` "
         "(or __graft_entry__.build()); there is no CPU fallback")
 
+try:
+    from . import _bind
+except ImportError as e:
+    raise ImportError("the extension module _bind is missing or does not load: build it with "
+                      f"`python -m ternary_weight_decoder_b200.build` ({e})") from e
+
 _lib = ctypes.CDLL(LIB_PATH)
 
 TW_OK = 0
@@ -503,99 +509,38 @@ tw_decoder_chain_cached = _sig("tw_decoder_chain_cached", _int,
                                [_p, _p, _int, _p, _p, _p, _sz, _p])
 
 
-# These calls stand between kernels of a few microseconds, so their checks read
-# each property of a tensor once and look for the words only to refuse it.
-_F32, _F64, _I32, _I8, _U8 = torch.float32, torch.float64, torch.int32, torch.int8, torch.uint8
-_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
-_empty_strided = torch.empty_strided
+# The calls of this section stand between kernels of a few microseconds, so
+# ``_bind`` (csrc/tw_bind.cpp) checks their tensors, makes their outputs and
+# calls the entry points named above on the tensors' device and its current
+# stream.
+_bind.init(TernaryError, *(ctypes.cast(f, _p).value for f in (
+    tw_kv_assign, tw_rope_append, tw_paged_attention, tw_paged_attention_workspace_bytes,
+    tw_residual_norm, tw_last_error)))
 
 
-def _launch(fn, index, stream, used, *args):
-    """Call ``fn(*args, raw_stream)`` on device ``index`` and raise on its
-    status.  With a stream other than the current one, the tensors in ``used``
-    are kept from reuse until that stream has passed this point."""
-    if index != _current_device():
-        with torch.cuda.device(index):
-            return _launch(fn, index, stream, used, *args)
-    if stream is None:
-        status = fn(*args, _raw_stream(index))
-        if status:
-            _raise(status)
-        return
-    status = fn(*args, stream.cuda_stream)
-    if status:
-        _raise(status)
-    if stream.cuda_stream != _raw_stream(index):
-        for t in used:
-            if t is not None:
-                t.record_stream(stream)
-
-
-def _new(beside, size, strides, dtype, stream):
-    """An output on the device of ``beside``, made on the stream that writes it."""
-    if stream is None:
-        return _empty_strided(size, strides, dtype=dtype, device=beside.device)
+def _on(stream, used, fn, *args):
+    """``fn(*args)`` on a stream of the caller's: the outputs are made on it,
+    and the tensors in ``used`` kept from reuse until it has passed this point."""
+    outer = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
-        return _empty_strided(size, strides, dtype=dtype, device=beside.device)
+        for t in used:
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+                raise ValueError(f"the stream is on {stream.device}, a tensor on {t.device}")
+        out = fn(*args)
+    if stream != outer:
+        for t in used:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return out
 
 
-def _refuse(t, dtype, shape, name, index):
-    """Say what is wrong with a tensor that has not this type, shape (None:
-    any size), device or memory order."""
+def _need_vector(t, dtype, n, name, index):
+    """A contiguous tensor of n elements (None: any) in one dimension."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a tensor of {dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
-    if len(t.shape) != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _device_of(t, name):
-    """Index of the CUDA device that a tensor is on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
-
-
-def _vector(t, dtype, n, name, index):
-    """A contiguous tensor of n elements in one dimension."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or \
-            t.shape != (n,) or not t.is_contiguous():
-        _refuse(t, dtype, (n,), name, index)
-
-
-def _rows(t, rows, width, name, index):
-    """An fp32 matrix whose rows are contiguous (any row stride); returns the stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.get_device() != index or \
-            t.shape != (rows, width):
-        _refuse(t, _F32, (rows, width), name, index)
-    if rows <= 1:
-        if width > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-        return -(-width // 4) * 4   # one row has no stride of its own
-    ld, step = t.stride()
-    if step != 1 and width > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return ld
-
-
-def _table(t, requests, index):
-    """A block table [requests, max_pages] with contiguous rows; returns (max_pages, row stride)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 2 or \
-            t.shape[0] != requests or t.get_device() != index:
-        _refuse(t, _I32, (requests, None), "block_table", index)
-    pages = t.shape[1]
-    if pages > 1 and t.stride(1) != 1:
-        raise ValueError("block_table must have contiguous rows")
-    return pages, t.stride(0) if requests > 1 else pages
-
-
-def _matrix(t, name):
-    """The shape of a two-dimensional tensor."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, has {t.dim()}")
-    return t.shape
+    if t.get_device() != index or t.dim() != 1 or n not in (None, t.shape[0]) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} on cuda:{index}, "
+                         f"is {list(t.shape)} on {t.device}")
 
 
 def _data(t):
@@ -611,8 +556,9 @@ class KVCache:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
-        self.index = _device_of(k, "k")
-        self.device = k.device
+        if not isinstance(k, torch.Tensor) or not k.is_cuda:
+            raise ValueError("k must be a CUDA tensor")
+        self.index, self.device = k.get_device(), k.device
         if k.dtype not in KV_DTYPES:
             raise TypeError(f"pools must be one of {list(KV_DTYPES)}, got {k.dtype}")
         if not isinstance(v, torch.Tensor) or k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or \
@@ -628,9 +574,9 @@ class KVCache:
             raise ValueError("int8 pools come with k_scale and v_scale, others without")
         if k_scale is not None:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.shape != k.shape[:3] or \
-                        t.get_device() != self.index or not t.is_contiguous():
-                    _refuse(t, _F32, k.shape[:3], name, self.index)
+                if t.dtype != torch.float32 or t.shape != k.shape[:3] or t.device != k.device or \
+                        not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous fp32 {list(k.shape[:3])} beside the pools")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         strides = [s or -(-self.head_dim // 16) * 16 for s in strides]
@@ -672,34 +618,10 @@ def kv_assign(lengths: torch.Tensor, delta: torch.Tensor, block_table: torch.Ten
     stride) and ``free_pages`` are updated in place, and each new token gets a
     row.  ``lengths_out`` and ``free_count_out`` may be the inputs themselves.
     A step that does not fit changes nothing and is reported by ``check``."""
-    index = _device_of(lengths, "lengths")
-    n = lengths.shape[0] if lengths.dim() else None
-    _vector(lengths, _I32, n, "lengths", index)
-    _vector(delta, _I32, n, "delta", index)
-    capacity = len(free_pages) if isinstance(free_pages, torch.Tensor) and free_pages.dim() else None
-    _vector(free_pages, _I32, capacity, "free_pages", index)
-    _vector(free_count, _I32, 1, "free_count", index)
-    width, stride = _table(block_table, n, index)
-    if rows < 0:
-        raise ValueError("rows must be >= 0")
-    if lengths_out is not None:
-        _vector(lengths_out, _I32, n, "lengths_out", index)
-    if free_count_out is not None:
-        _vector(free_count_out, _I32, 1, "free_count_out", index)
-    made = _new(lengths, (3 * rows + 2 * n + 2,), (1,), _I32, stream)
-    slots, positions, requests, row_start, new_lengths, new_count = made.split_with_sizes(
-        (rows, rows, rows, n + 1, n, 1))
-    if lengths_out is None:
-        lengths_out = new_lengths
-    if free_count_out is None:
-        free_count_out = new_count
-    at = made.data_ptr()
-    _launch(tw_kv_assign, index, stream,
-            (lengths, delta, block_table, free_pages, free_count, lengths_out, free_count_out, made),
-            lengths.data_ptr(), delta.data_ptr(), n, page_size, block_table.data_ptr(), width, stride,
-            free_pages.data_ptr(), capacity, free_count.data_ptr(), lengths_out.data_ptr(),
-            free_count_out.data_ptr(), at, at + 4 * rows, at + 8 * rows, rows, at + 12 * rows)
-    return KVAssignment(lengths_out, free_count_out, slots, positions, requests, row_start)
+    args = (lengths, delta, block_table, free_pages, free_count, page_size, rows, lengths_out, free_count_out)
+    if stream is not None:
+        return KVAssignment(*_on(stream, args, _bind.kv_assign, *args))
+    return KVAssignment(*_bind.kv_assign(*args))
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -709,33 +631,10 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     positions [rows] * inv_freq [rotary / 2] (fp64; None: no rotation), write
     k and v into the cache at slots [rows] (negative: not written) and return
     the rotated queries (``q_out``; may be q).  Rows may be strided."""
-    index = _device_of(q, "q")
-    rows, width = _matrix(q, "q")
-    dim = cache.head_dim
-    wide = cache.kv_heads * dim
-    heads = width // dim
-    if heads * dim != width:
-        raise ValueError(f"q has {width} columns, not whole heads of {dim}")
-    ldq = _rows(q, rows, width, "q", index)
-    ldk = _rows(k, rows, wide, "k", index)
-    ldv = _rows(v, rows, wide, "v", index)
-    _vector(positions, _I32, rows, "positions", index)
-    _vector(slots, _I32, rows, "slots", index)
-    if cache.index != index:
-        raise ValueError(f"the cache must be on cuda:{index}, is on {cache.device}")
-    rotary = freq = None
-    if inv_freq is not None and len(inv_freq):
-        rotary, freq = 2 * len(inv_freq), inv_freq.data_ptr()
-        _vector(inv_freq, _F64, rotary // 2, "inv_freq", index)
-    if q_out is None:
-        q_out = _new(q, (rows, width), (width, 1), _F32, stream)
-        ldqo = width
-    else:
-        ldqo = _rows(q_out, rows, width, "q_out", index)
-    _launch(tw_rope_append, index, stream, (q, k, v, positions, slots, inv_freq, q_out) + cache.tensors,
-            q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, heads, rotary or 0, freq,
-            interleaved, positions.data_ptr(), slots.data_ptr(), cache.ref, q_out.data_ptr(), ldqo)
-    return q_out
+    if stream is not None:
+        return _on(stream, (q, k, v, positions, slots, inv_freq, q_out) + cache.tensors, rope_append,
+                   q, k, v, positions, slots, cache, inv_freq, interleaved, q_out)
+    return _bind.rope_append(q, k, v, positions, slots, cache.ref, cache.index, inv_freq, interleaved, q_out)
 
 
 def paged_attention_workspace(requests: int, heads: int, cache: KVCache) -> torch.Tensor:
@@ -756,44 +655,11 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     [requests, max_pages]; scale is 1 / sqrt(head_dim) by default.  Returns out,
     or (out, lse) with the log-sum-exps [requests, heads].  ``ws`` comes from
     ``paged_attention_workspace`` (None: one is made for the call)."""
-    index = _device_of(q, "q")
-    n, width = _matrix(q, "q")
-    heads = width // cache.head_dim
-    if heads * cache.head_dim != width:
-        raise ValueError(f"q has {width} columns, not whole heads of {cache.head_dim}")
-    if cache.index != index:
-        raise ValueError(f"the cache must be on cuda:{index}, is on {cache.device}")
-    ldq = _rows(q, n, width, "q", index)
-    pages, stride = _table(block_table, n, index)
-    _vector(lengths, _I32, n, "lengths", index)
-    if first is not None:
-        _vector(first, _I32, n, "first", index)
-    if out is None:
-        out = _new(q, (n, width), (width, 1), _F32, stream)
-        ldo = width
-    else:
-        ldo = _rows(out, n, width, "out", index)
-    if lse is not None:
-        if not isinstance(lse, torch.Tensor) or lse.dtype is not _F32 or lse.get_device() != index or \
-                lse.shape != (n, heads) or not lse.is_contiguous():
-            _refuse(lse, _F32, (n, heads), "lse", index)
-    elif return_lse:
-        lse = _new(q, (n, heads), (heads, 1), _F32, stream)
-    if ws is None:
-        if stream is None:
-            ws = paged_attention_workspace(n, heads, cache)
-        else:
-            with torch.cuda.stream(stream):
-                ws = paged_attention_workspace(n, heads, cache)
-    size = len(ws)
-    _vector(ws, _U8, size, "ws", index)
-    if scale is None:
-        scale = cache.scale
-    _launch(tw_paged_attention, index, stream,
-            (q, block_table, lengths, first, out, lse, ws) + cache.tensors,
-            q.data_ptr(), ldq, n, heads, cache.ref, block_table.data_ptr(), pages, stride,
-            lengths.data_ptr(), _data(first), scale, out.data_ptr(), ldo, _data(lse), ws.data_ptr(), size)
-    return (out, lse) if return_lse else out
+    if stream is not None:
+        return _on(stream, (q, block_table, lengths, first, out, lse, ws) + cache.tensors, paged_attention,
+                   q, cache, block_table, lengths, first, scale, out, lse, ws, return_lse)
+    return _bind.paged_attention(q, cache.ref, cache.index, block_table, lengths, first,
+                                 cache.scale if scale is None else scale, out, lse, ws, return_lse)
 
 
 # -------------------------------------------- residual sum with its norms
@@ -821,56 +687,13 @@ def residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post: str |
     ``quantize`` gives the int8 codes of n (as ``quantize_act``) in its
     place, ready for ``ternary_linear_q``.  h and n may be passed in, h may be
     x and n may be y."""
-    index = _device_of(x, "x")
-    rows, width = _matrix(x, "x")
-    size = (rows, width)
-    ldx = _rows(x, rows, width, "x", index)
     if post not in NORMS or pre not in NORMS:
         raise ValueError(f"post and pre must be one of {list(NORMS)}")
-    ldy = 0 if y is None else _rows(y, rows, width, "y", index)
-    ldg = 0
-    if gate is not None:
-        if gate.dim() == 1:
-            _vector(gate, _F32, width, "gate", index)
-        else:
-            ldg = _rows(gate, rows, width, "gate", index)
-    if post_weight is not None:
-        _vector(post_weight, _F32, width, "post_weight", index)
-    if post_bias is not None:
-        _vector(post_bias, _F32, width, "post_bias", index)
-    if pre_weight is not None:
-        _vector(pre_weight, _F32, width, "pre_weight", index)
-    if pre_bias is not None:
-        _vector(pre_bias, _F32, width, "pre_bias", index)
-    ldh = ldn = 0
-    if h is not None:
-        ldh = _rows(h, rows, width, "h", index)
-    elif y is not None:
-        h = _new(x, size, (width, 1), _F32, stream)
-        ldh = width
-    # (neither: h is x as it stands)
-    xq = amax = qsum = None
-    if quantize:
-        if n is not None:
-            raise ValueError("quantize gives codes: n cannot be passed in")
-        xq = _new(x, size, (width, 1), _I8, stream)
-        amax = _new(x, (rows,), (1,), _F32, stream)
-        qsum = _new(x, (rows,), (1,), _I32, stream)
-    elif n is not None:
-        ldn = _rows(n, rows, width, "n", index)
-    elif pre is not None:
-        n = _new(x, size, (width, 1), _F32, stream)
-        ldn = width
-    elif h is None:
-        raise ValueError("nothing to compute: no y, no norm and no codes")
-    args = NormArgs(x.data_ptr(), _data(y), _data(gate), _data(post_weight), _data(post_bias),
-                    _data(pre_weight), _data(pre_bias), _data(h), _data(n), _data(xq), _data(amax),
-                    _data(qsum), rows, width, ldx, ldy, ldg, ldh, ldn, NORMS[post], NORMS[pre], alpha,
-                    eps)
-    _launch(tw_residual_norm, index, stream,
-            (x, y, gate, post_weight, post_bias, pre_weight, pre_bias, h, n, xq, amax, qsum),
-            ctypes.byref(args))
-    return NormResult(x if h is None else h, n, xq, amax, qsum)
+    args = (x, y, NORMS[post], post_weight, post_bias, gate, alpha, NORMS[pre], pre_weight, pre_bias, eps,
+            h, n, quantize)
+    if stream is not None:
+        return NormResult(*_on(stream, args, _bind.residual_norm, *args))
+    return NormResult(*_bind.residual_norm(*args))
 
 
 # ------------------------------------- decoder-layer chain with its cache
@@ -891,14 +714,18 @@ class CachedDecoderChain(DecoderChain):
         if len(caches) != len(layers) or len(norms) != len(layers):
             raise ValueError("one cache and one pair of norm gains per layer")
         dev, index = self.h.device, self.h.get_device()
-        for t, name in ((lengths, "lengths"), (positions, "positions"), (slots, "slots"), (first, "first")):
-            if t is not None or name != "first":
-                _vector(t, _I32, M, name, index)
-        pages, stride = _table(block_table, M, index)
+        for t, name in ((lengths, "lengths"), (positions, "positions"), (slots, "slots")):
+            _need_vector(t, torch.int32, M, name, index)
+        if first is not None:
+            _need_vector(first, torch.int32, M, "first", index)
         if inv_freq is not None:
-            _vector(inv_freq, _F64, len(inv_freq), "inv_freq", index)
+            _need_vector(inv_freq, torch.float64, None, "inv_freq", index)
         for t in [norm_out] + [t for pair in norms for t in pair]:
-            _vector(t, _F32, hidden, "norm gain", index)
+            _need_vector(t, torch.float32, hidden, "norm gain", index)
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != M or \
+                block_table.get_device() != index or not block_table.is_contiguous():
+            raise ValueError(f"block_table must be contiguous int32 [{M}, max_pages] on {dev}")
+        pages = stride = block_table.shape[1]
         for c in caches:
             if c.index != index:
                 raise ValueError(f"the caches must be on {dev}")
@@ -921,6 +748,7 @@ class CachedDecoderChain(DecoderChain):
 
 def decoder_chain_cached(chain: CachedDecoderChain, stream=None):
     """Run every layer of ``chain`` for one new token per request."""
-    _launch(tw_decoder_chain_cached, chain.h.get_device(), stream, (),
+    with torch.cuda.device(chain.h.device):
+        _raise(tw_decoder_chain_cached(
             chain.c_layers, chain.c_cached, chain.n_layers, ctypes.byref(chain.c_buf),
-            ctypes.byref(chain.c_cache), chain.ws.data_ptr(), chain.ws_bytes)
+            ctypes.byref(chain.c_cache), _ptr(chain.ws), chain.ws_bytes, _stream(stream)))
