@@ -18,7 +18,7 @@ namespace {
 
 // Sum (or maximum) over the threads of a row, in a fixed order: the lanes by
 // butterfly, then (a row of more than one warp) the warps' values in order.
-template <bool MAX, bool WARP>
+template <bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float *red, int warps)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -27,7 +27,7 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int warps)
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
         v = MAX ? fmaxf(v, u) : v + u;
     }
-    if (WARP)
+    if (warps == 1)
         return v;
     __syncthreads();   // the last reduction's values are read
     if (lane == 0)
@@ -56,19 +56,16 @@ template <> struct Vec<1> {
     static __device__ __forceinline__ void store(float *p, const float (&v)[1]) { *p = v[0]; }
 };
 
-// One row by a warp (blocks of kRows rows) or by a block: thread t of the
-// row's `threads` holds columns V * (t + i * threads) + 0 .. V - 1.
-constexpr int kRows = 4;
-template <int V, int PER, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(const ResidualNorm a)
+// One block a row: thread t holds columns V * (t + i * blockDim) + 0 .. V - 1.
+// Up to 512 threads the registers are kept to 64, so that two blocks share an
+// SM and one loads while the other reduces.
+template <int V, int PER, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const ResidualNorm a)
 {
     __shared__ float red[32];
     __shared__ int red_i[32];
-    const int threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int K = (int)a.K, warps = threads / 32;
-    const int64_t m = WARP ? (int64_t)blockIdx.x * kRows + (threadIdx.x >> 5) : blockIdx.x;
-    if (WARP && m >= a.M)
-        return;
+    const int threads = blockDim.x, tid = threadIdx.x, K = (int)a.K, warps = threads / 32;
+    const int64_t m = blockIdx.x;
     const float inv = 1.0f / (float)K;
     auto col = [&](int i) { return (i * threads + tid) * V; };
     auto read = [&](const float *row, float (&v)[PER][V]) {
@@ -100,7 +97,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(cons
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     s += v[i][j];
-            const float mean = row_reduce<false, WARP>(s, red, warps) * inv;
+            const float mean = row_reduce<false>(s, red, warps) * inv;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
 #pragma unroll
@@ -113,7 +110,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(cons
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 q = fmaf(v[i][j], v[i][j], q);
-        const float var = row_reduce<false, WARP>(q, red, warps) * inv;
+        const float var = row_reduce<false>(q, red, warps) * inv;
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -138,7 +135,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(cons
     float u[PER][V];
     if (a.y) {
         // x is on its way while y is normed, where the registers hold both
-        constexpr bool kAhead = WARP || PER * V <= 16;
+        constexpr bool kAhead = PER * V <= 20;
         float x[kAhead ? PER : 1][V];
         read(a.y + m * a.ldy, u);
         if constexpr (kAhead)
@@ -175,7 +172,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(cons
 #pragma unroll
         for (int j = 0; j < V; ++j)
             top = fmaxf(top, col(i) < K ? fabsf(u[i][j]) : 0.f);
-    top = row_reduce<true, WARP>(top, red, warps);
+    top = row_reduce<true>(top, red, warps);
     const float scale = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
     int sum = 0;
 #pragma unroll
@@ -198,14 +195,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(cons
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (!WARP) {
-            if ((tid & 31) == 0)
-                red_i[tid >> 5] = sum;
-            __syncthreads();
-            if (tid == 0)
-                for (int w = 1; w < warps; ++w)
-                    sum += red_i[w];
-        }
+        if ((tid & 31) == 0)
+            red_i[tid >> 5] = sum;
+        __syncthreads();
+        if (tid == 0)
+            for (int w = 1; w < warps; ++w)
+                sum += red_i[w];
         if (tid == 0)
             a.qsum[m] = sum;
     }
@@ -213,15 +208,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kRows : 1024) k_residual_norm(cons
         a.amax[m] = top;
 }
 
-template <int V, int PER, bool WARP>
+template <int V, int PER, int THREADS = 512>
 cudaError_t launch(const ResidualNorm &a, cudaStream_t stream)
 {
-    const int64_t groups = (a.K + V - 1) / V;
-    if (WARP)
-        k_residual_norm<V, PER, WARP><<<(unsigned)((a.M + kRows - 1) / kRows), 32 * kRows, 0, stream>>>(a);
-    else   // whole warps, PER groups a thread
-        k_residual_norm<V, PER, WARP><<<(unsigned)a.M, (unsigned)((groups + 32 * PER - 1) / (32 * PER) * 32), 0,
-                                        stream>>>(a);
+    // whole warps, PER groups a thread
+    const int64_t groups = (a.K + V - 1) / V, threads = (groups + 32 * PER - 1) / (32 * PER) * 32;
+    k_residual_norm<V, PER, THREADS><<<(unsigned)a.M, (unsigned)threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -238,16 +230,25 @@ cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
                        by16(a.post_w) && by16(a.post_b) && by16(a.pre_w) && by16(a.pre_b) &&
                        by16(a.h) && by16(a.n) && by16(a.xq);
     if (!quads) {
-        if (a.K <= 4096)
-            return launch<1, 4, false>(a, stream);
-        return a.K <= 8192 ? launch<1, 8, false>(a, stream) : launch<1, 32, false>(a, stream);
+        if (a.K <= 2048)
+            return launch<1, 4>(a, stream);
+        return a.K <= 8192 ? launch<1, 16>(a, stream) : launch<1, 32, 1024>(a, stream);
     }
+    // Threads to fill the row with as few groups each as 512 of them allow;
+    // two groups where there are rows enough (4096 rows of 1536: 20.9 us, with
+    // one 22.5 us), one for latency where there are not (2.1 / 2.4 us).
     const int64_t groups = a.K / 4;
     if (groups <= 512 && a.M < 148)
-        return launch<4, 1, false>(a, stream);
-    if (groups <= 1024)
-        return launch<4, 2, false>(a, stream);
-    return groups <= 4096 ? launch<4, 4, false>(a, stream) : launch<4, 8, false>(a, stream);
+        return launch<4, 1>(a, stream);
+    switch ((groups + 511) / 512) {
+    case 1: case 2: return launch<4, 2>(a, stream);
+    case 3: return launch<4, 3>(a, stream);
+    case 4: return launch<4, 4>(a, stream);
+    case 5: return launch<4, 5>(a, stream);
+    case 6: return launch<4, 6>(a, stream);
+    case 7: case 8: return launch<4, 8>(a, stream);
+    default: return launch<4, 8, 1024>(a, stream);
+    }
 }
 
 }  // namespace tw
