@@ -275,6 +275,7 @@ int check_chain_buffers(const tw_chain_buffers *b)
 }  // namespace
 
 namespace tw {
+unsigned long long context_id() { return current_context_id(); }
 int error_word(uint32_t **out) { return err_word(out); }
 int record_error(int code, const char *msg) { return fail(code, "%s", msg); }
 void clear_error() { t_last_error[0] = 0; }

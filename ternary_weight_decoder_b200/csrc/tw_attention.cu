@@ -33,7 +33,6 @@
 // 21.2 us of codes (6.7 TB/s), the memory's rate; what is left is the start
 // (scanning lengths, looking up pages, the first keys: about 5 us) and the
 // joins (2 to 6 us).
-#include <atomic>
 #include <cfloat>
 
 #include "tw_kv.cuh"
@@ -1058,15 +1057,11 @@ cudaError_t launch(const PagedAttention &p, uint32_t *err, cudaStream_t stream)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // The kernel's shared memory is asked for once per device, and again
-    // should a launch find it gone (a device that was reset).
-    static std::atomic<uint64_t> asked{0};
-    const uint64_t bit = 1ull << (dev & 63);
-    if (e == cudaSuccess && !(asked.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e == cudaSuccess)
-            asked.fetch_or(bit, std::memory_order_relaxed);
-    }
+    if (e == cudaSuccess)
+        e = ask_once([] {
+            return cudaFuncSetAttribute(k_paged_attention<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        S::kSmem);
+        });
     if (e != cudaSuccess)
         return e;
     const tw_kv_cache &c = p.cache;
@@ -1096,15 +1091,7 @@ cudaError_t launch(const PagedAttention &p, uint32_t *err, cudaStream_t stream)
     static_assert(kFan * 32 >= kMaxCtas && S::kWarps <= kFan, "a lane for each part");
     grid = grid < tiles ? grid : tiles;
     kernel<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a);
-    e = cudaGetLastError();
-    if (e == cudaErrorInvalidValue) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e == cudaSuccess) {
-            kernel<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a);
-            e = cudaGetLastError();
-        }
-    }
-    return e;
+    return cudaGetLastError();
 }
 
 template <int DT>

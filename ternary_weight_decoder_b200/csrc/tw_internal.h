@@ -337,6 +337,9 @@ constexpr int kMidGroup = TW_MID_GROUP;
 
 cudaError_t launch_wait_probe(uint32_t *err, uint64_t timeout_ns, cudaStream_t stream);
 
+// Id of the calling thread's current CUDA context (0: none), unique for the
+// life of the process.
+unsigned long long context_id();
 // Address of the per-device error word on the current device (TW_OK or a
 // TW_ERR_* status; the message is kept for tw_last_error()).
 int error_word(uint32_t **out);

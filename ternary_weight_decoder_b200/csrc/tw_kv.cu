@@ -15,8 +15,8 @@ namespace {
 
 // ------------------------------------------------------------- assignment
 constexpr int kAsThreads = 1024;
-constexpr int kAsCtas = 8;          // one portable cluster, or
-constexpr int64_t kAsSmall = 4096;  // a single block up to as many requests and rows
+constexpr int kAsCtas = 16;         // one cluster (of the largest size), or
+constexpr int64_t kAsSmall = 2800;  // a single block up to as many requests and rows
 
 __device__ __forceinline__ uint32_t pages_of(int32_t len, uint32_t page)   // len >= 0
 {
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t gtid = (int64_t)cluster.block_rank() * kAsThreads + tid;
     const int64_t gthreads = (int64_t)gridDim.x * kAsThreads;
+    const int64_t count = *a.free_count;
     if (tid == 0)
         bad = 0;
     __syncthreads();
@@ -113,7 +114,6 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
         if (lane == 31)
             total[warp] = w;
     }
-    const int64_t count = *a.free_count;
     __syncthreads();
     const int64_t top = count + total[2];   // height of the free list once pages are back
     uint32_t flags = bad;
@@ -174,24 +174,35 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
     }
     // rows, four in turn to a thread: one bisection, four loads in flight
     const int64_t used = ok ? total[0] : 0;
+    const bool quads = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions) |
+                         reinterpret_cast<uintptr_t>(a.request_of_row)) & 15) == 0;
     for (int64_t t0 = 4 * gtid; t0 < a.rows; t0 += 4 * gthreads) {
-        int32_t slot[4], pos[4], req[4];
+        int32_t page[4], in[4], pos[4], req[4], slot[4];
         int r = t0 < used ? owner(start, (int32_t)t0) : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t t = t0 + e;
-            slot[e] = -1, pos[e] = 0, req[e] = -1;
+            page[e] = in[e] = pos[e] = 0, req[e] = -1;
             if (t >= used)
                 continue;
             while (start[r + 1] <= t)   // (start[R] = used)
                 ++r;
             const int32_t p = old[r] + (int32_t)(t - start[r]);
             const int32_t held = (int32_t)pages_of(old[r], page_size), j = (int32_t)((uint32_t)p / page_size);
-            const int32_t page = j < held ? a.block_table[r * a.table_stride + j]
-                                          : a.free_pages[top - 1 - take[r] - (j - held)];
+            page[e] = *(j < held ? a.block_table + r * a.table_stride + j
+                                 : a.free_pages + (top - 1 - take[r] - (j - held)));
+            in[e] = (int32_t)((uint32_t)p - (uint32_t)j * page_size);
             req[e] = r;
             pos[e] = p;
-            slot[e] = (int32_t)(page * a.page_size + (p - j * a.page_size));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            slot[e] = req[e] < 0 ? -1 : (int32_t)(page[e] * a.page_size + in[e]);
+        if (quads && t0 + 4 <= a.rows) {
+            *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(a.request_of_row + t0) = make_int4(req[0], req[1], req[2], req[3]);
+            continue;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -444,14 +455,21 @@ cudaError_t launch_append(const RopeAppend &a, uint32_t *err, cudaStream_t strea
 cudaError_t launch_kv_assign(const KvAssign &a, uint32_t *err, cudaStream_t stream)
 {
     const size_t smem = (size_t)(4 * a.requests + 2) * sizeof(int32_t);
-    if (smem > 46 * 1024) {   // (with the static arrays, past the default limit)
-        cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)((4 * kAssignMaxRequests + 2) * sizeof(int32_t)));
+    const unsigned ctas = a.requests + a.rows <= kAsSmall ? 1 : kAsCtas;
+    if (ctas > 1) {   // the cluster's size and its shared memory are past what a kernel has without asking
+        cudaError_t e = ask_once(
+            [] {
+                cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                return e != cudaSuccess
+                           ? e
+                           : cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  (int)((4 * kAssignMaxRequests + 2) * sizeof(int32_t)));
+            });
         if (e != cudaSuccess)
             return e;
     }
+    static_assert((4 * kAsSmall + 2) * sizeof(int32_t) < 46 * 1024, "a single block needs no asking");
     cudaLaunchConfig_t cfg{};
-    const unsigned ctas = a.requests + a.rows <= kAsSmall ? 1 : kAsCtas;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kAsThreads);
     cfg.dynamicSmemBytes = smem;

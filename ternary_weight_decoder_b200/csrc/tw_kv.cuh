@@ -1,8 +1,8 @@
-// tw_kv.cuh — the paged key-value cache as the kernels see it, and the
-// conversions between its element types and fp32.
+// tw_kv.cuh — what the kernels of the paged key-value cache share.
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -12,14 +12,26 @@
 
 namespace tw {
 
-// Element types of the pools.
-template <int DT> struct KvElem;
-template <> struct KvElem<TW_KV_BF16> { using type = __nv_bfloat16; };
-template <> struct KvElem<TW_KV_F16> { using type = __half; };
-template <> struct KvElem<TW_KV_I8> { using type = int8_t; };
-
-__device__ __forceinline__ float kv_to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float kv_to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float kv_to_f32(int8_t v) { return (float)v; }
+// Run `ask` (what a kernel wants beyond the defaults: an attribute of a
+// function) once per device and context: after a device reset, whose context
+// has another id, it is asked again.  One cache per call site.
+template <class F>
+cudaError_t ask_once(F ask)
+{
+    static std::mutex mu;
+    static unsigned long long asked[SymbolCache::kDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long id = context_id();
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < SymbolCache::kDevices && id && asked[dev] == id)
+        return cudaSuccess;
+    e = ask();
+    if (e == cudaSuccess && dev < SymbolCache::kDevices)
+        asked[dev] = context_id();
+    return e;
+}
 
 }  // namespace tw

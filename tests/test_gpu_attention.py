@@ -10,7 +10,8 @@ from tests.test_gpu_kv import i32
 
 pytestmark = pytest.mark.gpu
 SHAPES = [(12, 2, 128), (2, 1, 128), (8, 8, 64), (14, 2, 64), (9, 3, 80), (8, 1, 256), (16, 1, 128),
-          (40, 2, 96), (1, 1, 16), (5, 5, 48), (20, 1, 256), (6, 2, 32)]
+          (40, 2, 96), (1, 1, 16), (5, 5, 48), (20, 1, 256), (6, 2, 32), (3, 1, 8), (4, 2, 24), (2, 1, 200),
+          (3, 3, 240), (32, 32, 64), (7, 1, 112)]
 
 
 @pytest.fixture(scope="module")
@@ -322,3 +323,65 @@ def test_step_in_a_graph(dev, api):
         assert torch.equal(out, w)
     api.check()
     assert torch.equal(graphed["lengths"], eager["lengths"]) and torch.equal(graphed["table"], eager["table"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "i8"])
+def test_attention_large_pages_and_all_heads(dev, api, dtype):
+    """Pages of more keys than a tile, and a layer of 64 query heads over one KV head."""
+    lengths = [3000, 700, 0, 4096, 4097]
+    for heads, hk, d, page in ((64, 1, 64, 2048), (16, 16, 128, 4096), (9, 3, 128, 1000)):
+        cache, q, table = make(api, dev, dtype, lengths, heads, hk, d, page, heads)
+        out, lse = api.paged_attention(G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev), return_lse=True)
+        api.check()
+        check_all(api, cache, q, table, lengths, None, out, lse, heads)
+
+
+def test_two_graphs_and_eager_share_a_workspace(dev, api):
+    """Captured calls of different shapes on one workspace, replayed in turn with eager ones on one stream."""
+    import torch
+    lengths = [9000, 17, 400]
+    ws, calls = None, []
+    for dtype, heads, hk, d in (("bf16", 12, 2, 128), ("i8", 8, 8, 64)):
+        cache, q, table = make(api, dev, dtype, lengths, heads, hk, d, 16, d)
+        args = (G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev))
+        ws = api.paged_attention_workspace(3, heads, cache) if ws is None else ws
+        want = api.paged_attention(*args, ws=ws)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            out = api.paged_attention(*args, ws=ws)
+        calls.append((g, out, want, args))
+    for _ in range(4):
+        for g, out, want, args in calls:
+            out.zero_()
+            g.replay()
+            assert torch.equal(out, want)
+            assert torch.equal(api.paged_attention(*args, ws=ws), want)
+    api.check()
+    assert int(ws[:3 * 512 * 8 * 4].any()) == 0   # the counters are zero again
+
+
+def test_attention_refuses_wrong_tensors(dev, api):
+    import torch
+    cache, q, table = make(api, dev, "bf16", [40, 20], 2, 1, 64, 16, 6)
+    x, t, n = G.to_dev(q, dev), i32(table, dev), i32([40, 20], dev)
+    good = (x, cache, t, n)
+    ok = api.paged_attention(*good)
+    for bad, kind in ((dict(q=x.double()), TypeError), (dict(q=x.cpu()), ValueError), (dict(q=x[0]), ValueError),
+                      (dict(q=x[:, :100]), ValueError), (dict(block_table=t.long()), TypeError),
+                      (dict(block_table=t[:1]), ValueError), (dict(block_table=t.t()), ValueError),
+                      (dict(lengths=n[:1]), ValueError), (dict(lengths=n.cpu()), ValueError), (dict(first=n.float()), TypeError),
+                      (dict(out=x[:, :64]), ValueError), (dict(out=x), api.TernaryError), (dict(lse=n), TypeError),
+                      (dict(ws=torch.zeros(16, dtype=torch.uint8, device=dev)), api.TernaryError),
+                      (dict(scale=float("inf")), api.TernaryError), (dict(scale="a"), TypeError)):
+        kw = dict(q=x, cache=cache, block_table=t, lengths=n)
+        kw.update(bad)
+        with pytest.raises(kind):
+            api.paged_attention(**kw)
+    assert torch.equal(api.paged_attention(*good), ok)
+    wide = torch.zeros(2, 2 ** 20, dtype=torch.int32, device=dev)   # 2 x 2^20 pages of 2^15 keys
+    big = api.KVCache(*[torch.zeros(1, 2 ** 15, 1, 64, dtype=torch.bfloat16, device=dev) for _ in range(2)])
+    many = torch.zeros(300, 64, device=dev)
+    with pytest.raises(api.TernaryError, match="too many"):
+        api.paged_attention(many, big, wide[:1].expand(300, 2 ** 20).contiguous(), i32([1] * 300, dev))
+    api.check()

@@ -192,3 +192,32 @@ def test_append_skips_bad_slots(dev, api):
     assert torch.equal(out, x)
     flat = cache.k.reshape(8, 16)
     assert torch.equal(flat[2], x[1].half()) and int((flat != 0).any(dim=1).sum()) == 1
+
+
+def test_kv_refuses_wrong_tensors(dev, api):
+    import torch
+    z, t = i32([0, 0], dev), i32([[0, 0], [0, 0]], dev)
+    good = dict(lengths=z, delta=i32([1, 1], dev), block_table=t, free_pages=i32([0, 1, 2], dev),
+                free_count=i32([3], dev), page_size=4, rows=4)
+    for bad, kind in ((dict(delta=z[:1]), ValueError), (dict(lengths=z.long()), TypeError), (dict(rows=-1), ValueError),
+                      (dict(block_table=t[:1]), ValueError), (dict(page_size=0), api.TernaryError),
+                      (dict(free_count=z), ValueError), (dict(delta=z), api.TernaryError), (dict(page_size="x"), TypeError),
+                      (dict(lengths_out=good["delta"]), api.TernaryError)):
+        with pytest.raises(kind):
+            api.kv_assign(**dict(good, **bad))
+    a = api.kv_assign(**good)
+    api.check()
+    assert a.slots.tolist() == [8, 4, -1, -1] and a.row_start.tolist() == [0, 1, 2]
+    cache = api.KVCache.empty(2, 4, 1, 16, torch.float16, dev)
+    x = torch.randn(2, 16, device=dev)
+    for bad, kind in ((dict(k=x[:, :8]), ValueError), (dict(positions=z.float()), TypeError), (dict(slots=z[:1]), ValueError),
+                      (dict(inv_freq=torch.ones(8, device=dev)), TypeError), (dict(q_out=x[:1]), ValueError),
+                      (dict(inv_freq=torch.ones(3, dtype=torch.float64, device=dev)), api.TernaryError), (dict(q=x[:, :12]), ValueError)):
+        kw = dict(q=x, k=x, v=x, positions=z, slots=i32([-1, -1], dev), cache=cache)
+        with pytest.raises(kind):
+            api.rope_append(**dict(kw, **bad))
+    for k, v in ((cache.k, cache.v[:1]), (cache.k.float(), cache.v.float()), (cache.k.transpose(2, 3), cache.v.transpose(2, 3))):
+        with pytest.raises((TypeError, ValueError)):
+            api.KVCache(k, v)
+    with pytest.raises(ValueError):
+        api.KVCache(torch.zeros(2, 4, 1, 16, dtype=torch.int8, device=dev), torch.zeros(2, 4, 1, 16, dtype=torch.int8, device=dev))

@@ -48,7 +48,8 @@ def _close(got, want, tol):
 
 
 @pytest.mark.parametrize("m,k", [(1, 1), (3, 2), (1, 1536), (32, 1536), (5, 1537), (2, 8960), (3, 8959),
-                                 (2, 32768), (2, 20001), (300, 64), (7, 130), (2, 16384)])
+                                 (2, 32768), (2, 20001), (300, 64), (7, 130), (2, 16384),
+                                 (150, 1536), (148, 4), (2, 4096), (2, 6000), (2, 8000), (2, 12000), (2, 14000), (2, 17000), (2, 3001)])
 @pytest.mark.parametrize("post,pre,gate", [(None, "rms", "none"), ("rms", "rms", "channel"),
                                            ("layer", "layer", "token"), ("rms", None, "token"),
                                            (None, "layer", "none")])
@@ -157,3 +158,30 @@ def test_codes_feed_a_projection(dev, api):
         b = api.ternary_linear(p.n, packed, wscale, 256)
         api.check()
         assert torch.equal(a, b)
+
+
+def test_norm_refuses_wrong_tensors(dev, api):
+    import torch
+    x, w = torch.randn(4, 256, device=dev), torch.ones(256, device=dev)
+    for kw, kind in ((dict(y=x.half()), TypeError), (dict(y=x[:2]), ValueError), (dict(y=x.cpu()), ValueError),
+                     (dict(y=x, gate=w[:8]), ValueError), (dict(pre_weight=w[:100]), ValueError), (dict(pre="batch"), ValueError),
+                     (dict(pre_weight=torch.ones(512, device=dev)[::2]), ValueError), (dict(pre=None), ValueError),
+                     (dict(quantize=True, n=x), ValueError), (dict(gate=w), api.TernaryError),
+                     (dict(pre_bias=w), api.TernaryError), (dict(y=x, h=x[:, :128]), ValueError),
+                     (dict(y=x, alpha=float("nan")), api.TernaryError), (dict(y=x, h=torch.zeros(1, 256, device=dev).expand(4, 256)), api.TernaryError)):
+        with pytest.raises(kind):
+            api.residual_norm(x, **kw)
+    with pytest.raises(ValueError):
+        api.residual_norm(x[0])
+    api.check()
+
+
+def test_norm_on_another_stream(dev, api):
+    import torch
+    x, y = torch.randn(64, 1536, device=dev), torch.randn(64, 1536, device=dev)
+    want = api.residual_norm(x, y)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [api.residual_norm(x, y, stream=s) for _ in range(10)]
+    s.synchronize()
+    assert all(torch.equal(g.n, want.n) and torch.equal(g.h, want.h) for g in got)
