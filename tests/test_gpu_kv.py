@@ -216,8 +216,12 @@ def test_kv_refuses_wrong_tensors(dev, api):
         kw = dict(q=x, k=x, v=x, positions=z, slots=i32([-1, -1], dev), cache=cache)
         with pytest.raises(kind):
             api.rope_append(**dict(kw, **bad))
-    for k, v in ((cache.k, cache.v[:1]), (cache.k.float(), cache.v.float()), (cache.k.transpose(2, 3), cache.v.transpose(2, 3))):
+    two = torch.zeros(2, 4, 2, 16, dtype=torch.float16, device=dev)
+    for k, v in ((cache.k, cache.v[:1]), (cache.k.float(), cache.v.float()), (two.transpose(2, 3), two.transpose(2, 3))):
         with pytest.raises((TypeError, ValueError)):
             api.KVCache(k, v)
     with pytest.raises(ValueError):
         api.KVCache(torch.zeros(2, 4, 1, 16, dtype=torch.int8, device=dev), torch.zeros(2, 4, 1, 16, dtype=torch.int8, device=dev))
+    with pytest.raises(api.TernaryError, match="head_dim"):   # pools of heads of one column
+        thin = api.KVCache(cache.k.transpose(2, 3), cache.v.transpose(2, 3))
+        api.rope_append(x, x, x, z, i32([-1, -1], dev), thin)
