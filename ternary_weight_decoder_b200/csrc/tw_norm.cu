@@ -8,36 +8,51 @@
 // The codes are those of tw_quantize_act on n, bit for bit.
 //
 // A row of x and y is read once and held in registers from then on; sums are
-// in 32 bits, the variance from the centred values.  Bound by memory: 16
-// bytes per element (x, y in; h, n out).
+// in 32 bits, the variance from the centred values.  Bound by memory, 16 bytes
+// per element (x, y in; h, n out): 4096 rows of 1536 with both norms and a
+// gate take 19.0 us (5.3 TB/s), of 8960 in 1000 rows 30.0 us (4.8 TB/s).
+// Measured and left out: persistent blocks with the next rows on their way
+// into shared memory (24.9 and 47.1 us: with one row at a time in a block the
+// reductions' latency shows), a warp a row (35.1 us at 1536).
 #include "tw_device.cuh"
 #include "tw_internal.h"
 
 namespace tw {
 namespace {
 
-// Sum (or maximum) over the threads of a row, in a fixed order: the lanes by
-// butterfly, then (a row of more than one warp) the warps' values in order.
-template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float *red, int warps)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+// Sums (or maxima) over the threads of a row, in a fixed order: the lanes by
+// butterfly, then the warps' values by butterfly in every warp.  The warps'
+// values of one reduction and the next go to different places, so that one
+// barrier each is enough.
+struct Reduction {
+    float (&red)[2][32];
+    int turn = 0;
+    template <bool MAX>
+    __device__ __forceinline__ static float butterfly(float v)
+    {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
-    }
-    if (warps == 1)
+        for (int o = 16; o; o >>= 1) {
+            const float u = __shfl_xor_sync(0xffffffffu, v, o);
+            v = MAX ? fmaxf(v, u) : v + u;
+        }
         return v;
-    __syncthreads();   // the last reduction's values are read
-    if (lane == 0)
-        red[warp] = v;
-    __syncthreads();
-    v = red[0];
-    for (int w = 1; w < warps; ++w)
-        v = MAX ? fmaxf(v, red[w]) : v + red[w];
-    return v;
-}
+    }
+    template <bool MAX>
+    __device__ __forceinline__ float over_row(float v, int warps)
+    {
+        const int lane = threadIdx.x & 31;
+        v = butterfly<MAX>(v);
+        if (warps == 1)
+            return v;
+        if (lane == 0)
+            red[turn][threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = lane < warps ? red[turn][lane] : 0.f;   // (0 is the least maximum of magnitudes too)
+        turn ^= 1;
+        return butterfly<MAX>(v);
+    }
+};
 
 template <int V> struct Vec;
 template <> struct Vec<4> {
@@ -56,30 +71,17 @@ template <> struct Vec<1> {
     static __device__ __forceinline__ void store(float *p, const float (&v)[1]) { *p = v[0]; }
 };
 
-// One block a row: thread t holds columns V * (t + i * blockDim) + 0 .. V - 1.
-// Up to 512 threads the registers are kept to 64, so that two blocks share an
-// SM and one loads while the other reduces.
-template <int V, int PER, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const ResidualNorm a)
+// The row that a block's threads hold in u (of y, or of x without y): its
+// norm, residual sum, norm and codes.  Thread t has columns
+// V * (t + i * blockDim) + 0 .. V - 1; x_at(i, v) and gate_at(i, v) give x and
+// the gate there.
+template <int V, int PER, class X, class G>
+__device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, float (&u)[PER][V], Reduction &sums,
+                                           int *red_i, X x_at, G gate_at)
 {
-    __shared__ float red[32];
-    __shared__ int red_i[32];
     const int threads = blockDim.x, tid = threadIdx.x, K = (int)a.K, warps = threads / 32;
-    const int64_t m = blockIdx.x;
     const float inv = 1.0f / (float)K;
     auto col = [&](int i) { return (i * threads + tid) * V; };
-    auto read = [&](const float *row, float (&v)[PER][V]) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (col(i) < K) {
-                Vec<V>::load(row + col(i), v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[i][j] = 0.f;
-            }
-        }
-    };
     auto write = [&](float *row, float (&v)[PER][V]) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     s += v[i][j];
-            const float mean = row_reduce<false>(s, red, warps) * inv;
+            const float mean = sums.over_row<false>(s, warps) * inv;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
 #pragma unroll
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 q = fmaf(v[i][j], v[i][j], q);
-        const float var = row_reduce<false>(q, red, warps) * inv;
+        const float var = sums.over_row<false>(q, warps) * inv;
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -132,30 +134,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const
         }
     };
 
-    float u[PER][V];
     if (a.y) {
-        // x is on its way while y is normed, where the registers hold both
-        constexpr bool kAhead = PER * V <= 20;
-        float x[kAhead ? PER : 1][V];
-        read(a.y + m * a.ldy, u);
-        if constexpr (kAhead)
-            read(a.x + m * a.ldx, x);
         norm(u, a.post, a.post_w, a.post_b);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (col(i) >= K)
                 continue;
-            float g[V];
+            float g[V], x[V];
             if (a.gate)
-                Vec<V>::load(a.gate + m * a.ldg + col(i), g);
-            if constexpr (!kAhead)
-                Vec<V>::load(a.x + m * a.ldx + col(i), x[0]);
+                gate_at(i, g);
+            x_at(i, x);
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                u[i][j] = fmaf(a.alpha, a.gate ? u[i][j] * g[j] : u[i][j], x[kAhead ? i : 0][j]);
+                u[i][j] = fmaf(a.alpha, a.gate ? u[i][j] * g[j] : u[i][j], x[j]);
         }
-    } else {
-        read(a.x + m * a.ldx, u);
     }
     if (a.h)
         write(a.h + m * a.ldh, u);
@@ -172,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const
 #pragma unroll
         for (int j = 0; j < V; ++j)
             top = fmaxf(top, col(i) < K ? fabsf(u[i][j]) : 0.f);
-    top = row_reduce<true>(top, red, warps);
+    top = sums.over_row<true>(top, warps);
     const float scale = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
     int sum = 0;
 #pragma unroll
@@ -198,14 +190,70 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_residual_norm(const
         if ((tid & 31) == 0)
             red_i[tid >> 5] = sum;
         __syncthreads();
-        if (tid == 0)
+        if (tid == 0) {
             for (int w = 1; w < warps; ++w)
                 sum += red_i[w];
-        if (tid == 0)
             a.qsum[m] = sum;
+        }
     }
     if (tid == 0)
         a.amax[m] = top;
+}
+
+// Blocks that share an SM: one loads while another reduces.  Three where a
+// thread has few columns (4096 rows of 1536: 19.0 us, two 20.3 us), else two
+// (1000 rows of 8960: 30.0 us; three would spill: 33.9 us).
+__host__ __device__ constexpr int blocks_of(int values, int threads) { return threads == 1024 ? 1 : values <= 16 ? 3 : 2; }
+
+// One block a row.
+template <int V, int PER, int THREADS>
+__global__ void __launch_bounds__(THREADS, blocks_of(V * PER, THREADS)) k_residual_norm(const ResidualNorm a)
+{
+    __shared__ float red[2][32];
+    __shared__ int red_i[32];
+    Reduction sums{red};
+    const int threads = blockDim.x, tid = threadIdx.x, K = (int)a.K;
+    const int64_t m = blockIdx.x;
+    auto col = [&](int i) { return (i * threads + tid) * V; };
+    auto read = [&](const float *row, auto &v) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (col(i) < K) {
+                Vec<V>::load(row + col(i), v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[i][j] = 0.f;
+            }
+        }
+    };
+    // x is on its way while y is normed: into registers where they hold both,
+    // else into L2
+    constexpr bool kAhead = V * PER <= 8 || (V * PER <= 20 && blocks_of(V * PER, THREADS) == 2);
+    float u[PER][V], x[kAhead ? PER : 1][V];
+    read((a.y ? a.y + m * a.ldy : a.x + m * a.ldx), u);
+    if (a.y) {
+        if constexpr (kAhead) {
+            read(a.x + m * a.ldx, x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (col(i) < K && (V > 1 || tid % 8 == 0))
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.x + m * a.ldx + col(i)));
+        }
+    }
+    finish_row<V, PER>(
+        a, m, u, sums, red_i,
+        [&](int i, float (&v)[V]) {
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = x[i][j];
+            } else {
+                Vec<V>::load(a.x + m * a.ldx + col(i), v);
+            }
+        },
+        [&](int i, float (&v)[V]) { Vec<V>::load(a.gate + m * a.ldg + col(i), v); });
 }
 
 template <int V, int PER, int THREADS = 512>
@@ -235,8 +283,8 @@ cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
         return a.K <= 8192 ? launch<1, 16>(a, stream) : launch<1, 32, 1024>(a, stream);
     }
     // Threads to fill the row with as few groups each as 512 of them allow;
-    // two groups where there are rows enough (4096 rows of 1536: 20.9 us, with
-    // one 22.5 us), one for latency where there are not (2.1 / 2.4 us).
+    // two groups where there are rows enough, one for latency where there are
+    // not (one row of 1536: 2.1 / 2.4 us).
     const int64_t groups = a.K / 4;
     if (groups <= 512 && a.M < 148)
         return launch<4, 1>(a, stream);
