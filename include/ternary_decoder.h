@@ -540,7 +540,9 @@ typedef struct tw_kv_cache {
  * length is negative or a count does not fit its array, TW_ERR_CORRUPT (both
  * returned by tw_check); then the table and the list are left as they were,
  * the lengths and the count are copied, every row gets -1, 0 and -1 and
- * row_start zeros.
+ * row_start zeros.  A row whose page, in the table or in the list, is negative
+ * or has slots past 2^31 gets slot -1, and TW_ERR_CORRUPT is recorded; the
+ * step is taken.
  * 1 <= requests <= 8192, 0 <= rows < 2^31.  One launch.
  */
 #define TW_KV_MAX_REQUESTS 8192

@@ -568,6 +568,8 @@ class KVCache:
         strides = [s if n > 1 else 0 for n, s in zip(k.shape, k.stride())]
         if strides != [s if n > 1 else 0 for n, s in zip(v.shape, v.stride())]:
             raise ValueError("k and v must have the same strides")
+        if any(n > 1 and s <= 0 for n, s in zip(k.shape, k.stride())):
+            raise ValueError("pools must not be expanded")
         if k.shape[3] > 1 and k.stride(3) != 1:
             raise ValueError("the head dimension of the pools must be contiguous")
         if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):

@@ -100,7 +100,7 @@ struct Shape {
     static constexpr int kTile = kKeys * kWarps;
     static constexpr int kBlocks = DP > 128 ? 1 : 2;   // resident on an SM
     static constexpr int kQueryBytes = kQuerySteps * kQueryParts * 32 * 8;   // a unit's queries, as operands
-    static constexpr int kRoom = (227 * 1024) / kBlocks - 3072 - kQueryBytes;
+    static constexpr int kRoom = (227 * 1024) / kBlocks - 3 * 1024 - kQueryBytes;
     static constexpr int kFit = kRoom / (kWarps * (kStage + kScales));
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kWarps * kStages * (kStage + kScales) + kQueryBytes;

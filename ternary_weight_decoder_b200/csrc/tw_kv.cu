@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
         return l;
     };
     // pages handed back, on top of the list
-    const int32_t given = ok ? (int32_t)total[2] : 0, taken = ok ? (int32_t)total[1] : 0;
-    for (int32_t k = (int32_t)gtid; k < given; k += (int32_t)gthreads) {
-        const int r = owner(give, k);
+    const int64_t given = ok ? total[2] : 0, taken = ok ? total[1] : 0;
+    for (int64_t k = gtid; k < given; k += gthreads) {
+        const int r = owner(give, (int32_t)k);
         // the last of its pages: entry `held` less those that are still to come
         const int64_t held = pages_of(old[r], page_size);
         a.free_pages[count + k] = a.block_table[r * a.table_stride + held - (give[r + 1] - k)];
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
     // Orders the list's new entries, and every read of the inputs that the
     // outputs may overwrite, before what follows in any block.
     cluster.sync();
-    for (int32_t k = (int32_t)gtid; k < taken; k += (int32_t)gthreads) {
-        const int r = owner(take, k);
+    for (int64_t k = gtid; k < taken; k += gthreads) {
+        const int r = owner(take, (int32_t)k);
         const int64_t held = pages_of(old[r], page_size);
         a.block_table[r * a.table_stride + held + (k - take[r])] = a.free_pages[top - 1 - k];
     }
@@ -196,8 +196,12 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
             pos[e] = p;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            slot[e] = req[e] < 0 ? -1 : (int32_t)(page[e] * a.page_size + in[e]);
+        for (int e = 0; e < 4; ++e) {
+            const int64_t s = page[e] * a.page_size + in[e];
+            if (page[e] < 0 || s > INT32_MAX)   // no page of any pool: a table or list that holds something else
+                atomicOr(err, EFLAG_BADDESC);
+            slot[e] = req[e] < 0 || page[e] < 0 || s > INT32_MAX ? -1 : (int32_t)s;
+        }
         if (quads && t0 + 4 <= a.rows) {
             *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
             *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);

@@ -385,3 +385,25 @@ def test_attention_refuses_wrong_tensors(dev, api):
     with pytest.raises(api.TernaryError, match="too many"):
         api.paged_attention(many, big, wide[:1].expand(300, 2 ** 20).contiguous(), i32([1] * 300, dev))
     api.check()
+
+
+def test_pools_with_strides_past_32_bits(dev, api):
+    """Two pages 2^32 bytes apart: appended to, then attended over, as in a dense pool."""
+    import torch
+    d, page, far = 64, 16, 2 ** 32
+    pools = [torch.zeros(far + page * d, dtype=torch.int8, device=dev).as_strided((2, page, 1, d), (far, d, d, 1)) for _ in range(2)]
+    scales = [torch.zeros(2, page, 1, device=dev) for _ in range(4)]
+    cache = api.KVCache(*pools, *scales[:2])
+    dense = api.KVCache(*[torch.zeros(2, page, 1, d, dtype=torch.int8, device=dev) for _ in range(2)], *scales[2:])
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    x = torch.randn(31, d, device=dev, generator=g)
+    inv = G.to_dev(100.0 ** (-np.arange(32) / 32.0), dev)
+    slots = i32(list(range(16, 32)) + list(range(15)), dev)
+    outs = []
+    for c in (cache, dense):
+        q = api.rope_append(x, x, x, i32(range(31), dev), slots, c, inv_freq=inv)
+        outs.append(api.paged_attention(q[:1], c, i32([[1, 0]], dev), i32([31], dev)))
+    api.check()
+    assert torch.equal(outs[0], outs[1]) and float(outs[0].abs().max()) > 0
+    assert torch.equal(cache.k[1], dense.k[1]) and torch.equal(cache.v[0], dense.v[0])

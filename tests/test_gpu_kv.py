@@ -225,3 +225,14 @@ def test_kv_refuses_wrong_tensors(dev, api):
     with pytest.raises(api.TernaryError, match="head_dim"):   # pools of heads of one column
         thin = api.KVCache(cache.k.transpose(2, 3), cache.v.transpose(2, 3))
         api.rope_append(x, x, x, z, i32([-1, -1], dev), thin)
+    with pytest.raises(ValueError, match="expanded"):
+        api.KVCache(cache.k.expand(2, 4, 3, 16), cache.v.expand(2, 4, 3, 16))
+
+
+def test_assign_flags_pages_that_are_none(dev, api):
+    """A row whose page, in the table or in the list, cannot be one gets no slot; the other rows do."""
+    for table, free in (([[-5, 0], [3, 0]], [1, 2]), ([[7, 0], [3, 0]], [1, 2 ** 30])):
+        a = api.kv_assign(i32([3, 2], dev), i32([2, 1], dev), i32(table, dev), i32(free, dev), i32([2], dev), 4, 3)
+        with pytest.raises(api.TernaryError, match="TW_ERR_CORRUPT"):
+            api.check()
+        assert a.slots.tolist() == ([-1, 8, 14] if table[0][0] < 0 else [31, -1, 14])
