@@ -460,18 +460,19 @@ cudaError_t launch_kv_assign(const KvAssign &a, uint32_t *err, cudaStream_t stre
 {
     const size_t smem = (size_t)(4 * a.requests + 2) * sizeof(int32_t);
     const unsigned ctas = a.requests + a.rows <= kAsSmall ? 1 : kAsCtas;
-    if (ctas > 1) {   // the cluster's size and its shared memory are past what a kernel has without asking
-        cudaError_t e = ask_once(
-            [] {
-                cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-                return e != cudaSuccess
-                           ? e
-                           : cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  (int)((4 * kAssignMaxRequests + 2) * sizeof(int32_t)));
-            });
-        if (e != cudaSuccess)
-            return e;
+    if (ctas == 1) {   // (a block of its own is a cluster of one)
+        k_kv_assign<<<1, kAsThreads, smem, stream>>>(a, err);
+        return cudaGetLastError();
     }
+    // the cluster's size and its shared memory are past what a kernel has without asking
+    cudaError_t e = ask_once([] {
+        cudaError_t e = cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(k_kv_assign, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)((4 * kAssignMaxRequests + 2) * sizeof(int32_t)));
+    });
+    if (e != cudaSuccess)
+        return e;
     static_assert((4 * kAsSmall + 2) * sizeof(int32_t) < 46 * 1024, "a single block needs no asking");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
