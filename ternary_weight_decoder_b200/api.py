@@ -706,7 +706,10 @@ class CachedDecoderChain(DecoderChain):
     ``norms`` one (norm_in, norm_mid) pair of gains per layer, ``norm_out``
     the last gain.  ``block_table`` [M, max_pages], ``lengths`` [M] (counting
     the new token), ``positions`` [M] and ``slots`` [M] are int32 tensors that
-    every run reads, as ``kv_assign`` fills them for one new token each."""
+    every run reads, row r for request r, as ``kv_assign`` fills them for one
+    new token each.  Where some requests take none, its rows are packed:
+    request r's slot is then ``slots[row_start[r]]`` if it took a token and -1
+    if it did not (its row still runs, and changes no cache)."""
 
     def __init__(self, layers, M: int, hidden: int, kv_dim: int, head_dim: int, inter: int, device,
                  caches, norms, norm_out, inv_freq, block_table, lengths, positions, slots,
