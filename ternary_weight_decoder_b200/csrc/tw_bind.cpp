@@ -8,6 +8,7 @@
 #include <string>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -144,9 +145,12 @@ float real(PyObject *o, const char *name)
     return (float)v;
 }
 
+// Outputs are made below the dispatcher, and parts of one buffer below the
+// tracking of views (the parts do not overlap and each is an output of its
+// own): kv_assign took 8.9 us with both, 7.2 without.
 at::Tensor make(at::IntArrayRef size, at::ScalarType type, const at::Tensor &beside)
 {
-    return at::empty(size, beside.options().dtype(type));
+    return at::Tensor(at::detail::empty_cuda(size, type, beside.device(), std::nullopt));
 }
 
 // Device `index`, made current for the call, and its current stream.
@@ -222,6 +226,7 @@ PyObject *kv_assign(PyObject *, PyObject *const *a, Py_ssize_t n_args)
                                  free_count.data_ptr<int32_t>(), lengths_out ? lengths_out : own,
                                  count_out ? count_out : own + n, p, p + count, p + 2 * count, count, starts,
                                  place.stream));
+        at::AutoDispatchBelowADInplaceOrView no_views;
         auto part = [&](int64_t at, int64_t size) { return made.as_strided({size}, {1}, at); };
         const int64_t s = 3 * count;
         return Py_BuildValue("(NNNNNN)", THPVariable_Wrap(lengths_out ? given_or(a[7], made) : part(s + n + 1, n)),
