@@ -73,13 +73,13 @@ template <> struct Vec<1> {
 
 // The row that a block's threads hold in u (of y, or of x without y): its
 // norm, residual sum, norm and codes.  Thread t has columns
-// V * (t + i * blockDim) + 0 .. V - 1; x_at(i, v) and gate_at(i, v) give x and
+// V * (t + i * STRIDE) + 0 .. V - 1 (STRIDE 0: blockDim); x_at(i, v) and gate_at(i, v) give x and
 // the gate there.
-template <int V, int PER, class X, class G>
+template <int V, int PER, int STRIDE, class X, class G>
 __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, float (&u)[PER][V], Reduction &sums,
                                            int *red_i, X x_at, G gate_at)
 {
-    const int threads = blockDim.x, tid = threadIdx.x, K = (int)a.K, warps = threads / 32;
+    const int threads = STRIDE ? STRIDE : blockDim.x, tid = threadIdx.x, K = (int)a.K, warps = threads / 32;
     const float inv = 1.0f / (float)K;
     auto col = [&](int i) { return (i * threads + tid) * V; };
     auto write = [&](float *row, float (&v)[PER][V]) {
@@ -205,14 +205,14 @@ __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, flo
 // (1000 rows of 8960: 30.0 us; three would spill: 33.9 us).
 __host__ __device__ constexpr int blocks_of(int values, int threads) { return threads == 1024 ? 1 : values <= 16 ? 3 : 2; }
 
-// One block a row.
-template <int V, int PER, int THREADS>
-__global__ void __launch_bounds__(THREADS, blocks_of(V * PER, THREADS)) k_residual_norm(const ResidualNorm a)
+// One block a row: of THREADS threads (STRIDE), or of as many as fill it.
+template <int V, int PER, int THREADS, int STRIDE, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) k_residual_norm(const ResidualNorm a)
 {
     __shared__ float red[2][32];
     __shared__ int red_i[32];
     Reduction sums{red};
-    const int threads = blockDim.x, tid = threadIdx.x, K = (int)a.K;
+    const int threads = STRIDE ? STRIDE : blockDim.x, tid = threadIdx.x, K = (int)a.K;
     const int64_t m = blockIdx.x;
     auto col = [&](int i) { return (i * threads + tid) * V; };
     auto read = [&](const float *row, auto &v) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of(V * PER, THREADS)) k_residu
     };
     // x is on its way while y is normed: into registers where they hold both,
     // else into L2
-    constexpr bool kAhead = V * PER <= 8 || (V * PER <= 20 && blocks_of(V * PER, THREADS) == 2);
+    constexpr bool kAhead = V * PER <= 8 || (V * PER <= 20 && BLOCKS * THREADS <= 1024);
     float u[PER][V], x[kAhead ? PER : 1][V];
     read((a.y ? a.y + m * a.ldy : a.x + m * a.ldx), u);
     if (a.y) {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of(V * PER, THREADS)) k_residu
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.x + m * a.ldx + col(i)));
         }
     }
-    finish_row<V, PER>(
+    finish_row<V, PER, STRIDE>(
         a, m, u, sums, red_i,
         [&](int i, float (&v)[V]) {
             if constexpr (kAhead) {
@@ -256,12 +256,20 @@ __global__ void __launch_bounds__(THREADS, blocks_of(V * PER, THREADS)) k_residu
         [&](int i, float (&v)[V]) { Vec<V>::load(a.gate + m * a.ldg + col(i), v); });
 }
 
-template <int V, int PER, int THREADS = 512>
+template <int V, int PER, int THREADS = 512, int BLOCKS = blocks_of(V * PER, THREADS)>
 cudaError_t launch(const ResidualNorm &a, cudaStream_t stream)
 {
     // whole warps, PER groups a thread
     const int64_t groups = (a.K + V - 1) / V, threads = (groups + 32 * PER - 1) / (32 * PER) * 32;
-    k_residual_norm<V, PER, THREADS><<<(unsigned)a.M, (unsigned)threads, 0, stream>>>(a);
+    k_residual_norm<V, PER, THREADS, 0, BLOCKS><<<(unsigned)a.M, (unsigned)threads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// Every thread of THREADS, its groups a constant apart.
+template <int V, int PER, int THREADS, int BLOCKS = blocks_of(V * PER, THREADS)>
+cudaError_t launch_all(const ResidualNorm &a, cudaStream_t stream)
+{
+    k_residual_norm<V, PER, THREADS, THREADS, BLOCKS><<<(unsigned)a.M, THREADS, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -278,24 +286,50 @@ cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
                        by16(a.post_w) && by16(a.post_b) && by16(a.pre_w) && by16(a.pre_b) &&
                        by16(a.h) && by16(a.n) && by16(a.xq);
     if (!quads) {
+        if (a.M < 148) {
+            if (a.K <= 1024)
+                return launch<1, 1, 1024>(a, stream);
+            if (a.K <= 2048)
+                return launch<1, 2, 1024>(a, stream);
+            if (a.K <= 4096)
+                return launch_all<1, 4, 1024>(a, stream);
+            if (a.K <= 8192)
+                return launch_all<1, 8, 1024>(a, stream);
+        }
         if (a.K <= 2048)
             return launch<1, 4>(a, stream);
-        return a.K <= 8192 ? launch<1, 16>(a, stream) : launch<1, 32, 1024>(a, stream);
+        if (a.K <= 2560)
+            return launch_all<1, 5, 512>(a, stream);
+        if (a.K <= 4096)
+            return launch_all<1, 8, 512>(a, stream);
+        if (a.K <= 6144)
+            return launch_all<1, 12, 512, 2>(a, stream);
+        if (a.K <= 8192)
+            return launch_all<1, 16, 512, 2>(a, stream);
+        return a.K <= 16384 ? launch_all<1, 16, 1024>(a, stream) : launch_all<1, 32, 1024>(a, stream);
     }
     // Threads to fill the row with as few groups each as 512 of them allow;
     // two groups where there are rows enough, one for latency where there are
     // not (one row of 1536: 2.1 / 2.4 us).
     const int64_t groups = a.K / 4;
-    if (groups <= 512 && a.M < 148)
-        return launch<4, 1>(a, stream);
+    if (a.M < 148) {
+        if (groups <= 512)
+            return launch<4, 1>(a, stream);
+        if (groups <= 1024)
+            return launch<4, 1, 1024>(a, stream);
+        if (groups <= 2048)
+            return launch<4, 2, 1024>(a, stream);
+        if (groups <= 4096)
+            return launch_all<4, 4, 1024>(a, stream);
+    }
     switch ((groups + 511) / 512) {
     case 1: case 2: return launch<4, 2>(a, stream);
     case 3: return launch<4, 3>(a, stream);
     case 4: return launch<4, 4>(a, stream);
     case 5: return launch<4, 5>(a, stream);
     case 6: return launch<4, 6>(a, stream);
-    case 7: case 8: return launch<4, 8>(a, stream);
-    default: return launch<4, 8, 1024>(a, stream);
+    case 7: case 8: return launch_all<4, 8, 512>(a, stream);
+    default: return launch_all<4, 8, 1024>(a, stream);
     }
 }
 
