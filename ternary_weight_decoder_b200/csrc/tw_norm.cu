@@ -200,10 +200,11 @@ __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, flo
         a.amax[m] = top;
 }
 
-// Blocks that share an SM: one loads while another reduces.  Three where a
-// thread has few columns (4096 rows of 1536: 19.0 us, two 20.3 us), else two
-// (1000 rows of 8960: 30.0 us; three would spill: 33.9 us).
-__host__ __device__ constexpr int blocks_of(int values, int threads) { return threads == 1024 ? 1 : values <= 16 ? 3 : 2; }
+// Blocks that share an SM, so that one loads while another reduces: of 512
+// threads three where a thread has few columns (4096 rows of 1536: 19.0 us, two
+// 20.3 us), else two (1000 rows of 8960: 30.0 us; three would spill: 33.9 us).
+template <int VALUES, int THREADS>
+constexpr int kBlocks = (VALUES <= 16 && THREADS <= 512 ? 1536 : 1024) / THREADS;
 
 // One block a row: of THREADS threads (STRIDE), or of as many as fill it.
 template <int V, int PER, int THREADS, int STRIDE, int BLOCKS>
@@ -228,19 +229,23 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_residual_norm(const Residua
         }
     };
     // x is on its way while y is normed: into registers where they hold both,
-    // else into L2
+    // else into L2, as a gate per token
+    auto ahead = [&](const float *row) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (col(i) < K && (V > 1 || tid % 8 == 0))
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(row + col(i)));
+    };
     constexpr bool kAhead = V * PER <= 8 || (V * PER <= 20 && BLOCKS * THREADS <= 1024);
     float u[PER][V], x[kAhead ? PER : 1][V];
     read((a.y ? a.y + m * a.ldy : a.x + m * a.ldx), u);
     if (a.y) {
-        if constexpr (kAhead) {
+        if constexpr (kAhead)
             read(a.x + m * a.ldx, x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (col(i) < K && (V > 1 || tid % 8 == 0))
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.x + m * a.ldx + col(i)));
-        }
+        else
+            ahead(a.x + m * a.ldx);
+        if (a.gate && a.ldg)
+            ahead(a.gate + m * a.ldg);
     }
     finish_row<V, PER, STRIDE>(
         a, m, u, sums, red_i,
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_residual_norm(const Residua
         [&](int i, float (&v)[V]) { Vec<V>::load(a.gate + m * a.ldg + col(i), v); });
 }
 
-template <int V, int PER, int THREADS = 512, int BLOCKS = blocks_of(V * PER, THREADS)>
+template <int V, int PER, int THREADS = 512, int BLOCKS = kBlocks<V * PER, THREADS>>
 cudaError_t launch(const ResidualNorm &a, cudaStream_t stream)
 {
     // whole warps, PER groups a thread
@@ -265,8 +270,10 @@ cudaError_t launch(const ResidualNorm &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-// Every thread of THREADS, its groups a constant apart.
-template <int V, int PER, int THREADS, int BLOCKS = blocks_of(V * PER, THREADS)>
+// Every thread of THREADS, its groups a constant apart: where they are many,
+// addresses and bounds of any other distance would not fit the registers (by
+// single columns 1280 rows of 4687: 32 us, 69 us).
+template <int V, int PER, int THREADS, int BLOCKS = kBlocks<V * PER, THREADS>>
 cudaError_t launch_all(const ResidualNorm &a, cudaStream_t stream)
 {
     k_residual_norm<V, PER, THREADS, THREADS, BLOCKS><<<(unsigned)a.M, THREADS, 0, stream>>>(a);
@@ -275,42 +282,11 @@ cudaError_t launch_all(const ResidualNorm &a, cudaStream_t stream)
 
 bool by16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-}  // namespace
-
-cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
+// Rows too few for every SM get threads enough for one group of columns each,
+// for latency (one row of 1536: 2.1 us, with two groups a thread 2.4; of 16384
+// with four groups 6.7, with eight 9.8).
+cudaError_t launch_quads(const ResidualNorm &a, cudaStream_t stream)
 {
-    // Groups of four columns where every row of every operand starts on a
-    // 16-byte boundary, single columns elsewhere (odd widths, odd strides).
-    const bool quads = a.K % 4 == 0 && a.ldx % 4 == 0 && a.ldy % 4 == 0 && a.ldg % 4 == 0 &&
-                       a.ldh % 4 == 0 && a.ldn % 4 == 0 && by16(a.x) && by16(a.y) && by16(a.gate) &&
-                       by16(a.post_w) && by16(a.post_b) && by16(a.pre_w) && by16(a.pre_b) &&
-                       by16(a.h) && by16(a.n) && by16(a.xq);
-    if (!quads) {
-        if (a.M < 148) {
-            if (a.K <= 1024)
-                return launch<1, 1, 1024>(a, stream);
-            if (a.K <= 2048)
-                return launch<1, 2, 1024>(a, stream);
-            if (a.K <= 4096)
-                return launch_all<1, 4, 1024>(a, stream);
-            if (a.K <= 8192)
-                return launch_all<1, 8, 1024>(a, stream);
-        }
-        if (a.K <= 2048)
-            return launch<1, 4>(a, stream);
-        if (a.K <= 2560)
-            return launch_all<1, 5, 512>(a, stream);
-        if (a.K <= 4096)
-            return launch_all<1, 8, 512>(a, stream);
-        if (a.K <= 6144)
-            return launch_all<1, 12, 512, 2>(a, stream);
-        if (a.K <= 8192)
-            return launch_all<1, 16, 512, 2>(a, stream);
-        return a.K <= 16384 ? launch_all<1, 16, 1024>(a, stream) : launch_all<1, 32, 1024>(a, stream);
-    }
-    // Threads to fill the row with as few groups each as 512 of them allow;
-    // two groups where there are rows enough, one for latency where there are
-    // not (one row of 1536: 2.1 / 2.4 us).
     const int64_t groups = a.K / 4;
     if (a.M < 148) {
         if (groups <= 512)
@@ -322,6 +298,7 @@ cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
         if (groups <= 4096)
             return launch_all<4, 4, 1024>(a, stream);
     }
+    // as few groups a thread as 512 threads allow, two at least
     switch ((groups + 511) / 512) {
     case 1: case 2: return launch<4, 2>(a, stream);
     case 3: return launch<4, 3>(a, stream);
@@ -331,6 +308,56 @@ cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
     case 7: case 8: return launch_all<4, 8, 512>(a, stream);
     default: return launch_all<4, 8, 1024>(a, stream);
     }
+}
+
+cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
+{
+    if (a.M < 148) {
+        if (a.K <= 1024)
+            return launch<1, 1, 1024>(a, stream);
+        if (a.K <= 2048)
+            return launch<1, 2, 1024>(a, stream);
+        if (a.K <= 4096)
+            return launch_all<1, 4, 1024>(a, stream);
+        if (a.K <= 8192)
+            return launch_all<1, 8, 1024>(a, stream);
+    }
+    // eight columns a thread (3903 rows of 1537: 26 us, four 39 us), more in
+    // rows that 512 threads cannot hold so
+    if (a.K <= 256)
+        return launch_all<1, 2, 128>(a, stream);
+    if (a.K <= 512)
+        return launch_all<1, 4, 128>(a, stream);
+    if (a.K <= 1024)
+        return launch_all<1, 8, 128>(a, stream);
+    if (a.K <= 1536)
+        return launch_all<1, 8, 192>(a, stream);
+    if (a.K <= 2048)
+        return launch_all<1, 8, 256>(a, stream);
+    if (a.K <= 2560)
+        return launch_all<1, 8, 320>(a, stream);
+    if (a.K <= 4096)
+        return launch_all<1, 8, 512>(a, stream);
+    if (a.K <= 6144)
+        return launch_all<1, 12, 512, 2>(a, stream);
+    if (a.K <= 8192)
+        return launch_all<1, 16, 512, 2>(a, stream);
+    return a.K <= 16384 ? launch_all<1, 16, 1024>(a, stream) : launch_all<1, 32, 1024>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
+{
+    // Groups of four columns where every row of every operand starts on a
+    // 16-byte boundary, single columns elsewhere (odd widths, odd strides).
+    const bool quads = a.K % 4 == 0 && a.ldx % 4 == 0 && a.ldy % 4 == 0 && a.ldg % 4 == 0 &&
+                       a.ldh % 4 == 0 && a.ldn % 4 == 0 && by16(a.x) && by16(a.y) && by16(a.gate) &&
+                       by16(a.post_w) && by16(a.post_b) && by16(a.pre_w) && by16(a.pre_b) &&
+                       by16(a.h) && by16(a.n) && by16(a.xq);
+    if (!quads)
+        return launch_singles(a, stream);
+    return launch_quads(a, stream);
 }
 
 }  // namespace tw
