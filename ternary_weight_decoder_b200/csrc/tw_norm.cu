@@ -324,8 +324,8 @@ cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
     }
     // eight columns a thread (3903 rows of 1537: 26 us, four 39 us), more in
     // rows that 512 threads cannot hold so
-    if (a.K <= 256)
-        return launch_all<1, 2, 128>(a, stream);
+    if (a.K <= 256)   // a warp a row where there are rows enough (4096 of 171: 5.9 us, 128 threads 7.5; 300: 4.1, 3.0)
+        return a.M > 12 * 148 ? launch_all<1, 8, 32, 32>(a, stream) : launch_all<1, 2, 128>(a, stream);
     if (a.K <= 512)
         return launch_all<1, 4, 128>(a, stream);
     if (a.K <= 1024)
