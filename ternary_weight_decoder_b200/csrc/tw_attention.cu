@@ -14,8 +14,8 @@
 // to end, and every block takes an equal run of them, whatever the lengths
 // are.  A block whose run holds all of a (request, KV head) writes its
 // output; the pieces of one that spans blocks go to the workspace and are
-// joined in a fixed order, each head by the warp that finishes it last, kFan
-// pieces at a time and then those.  Inside a block each warp takes 16 keys (32
+// joined in a fixed order, each head by the half warp that finishes it last,
+// kFan pieces at a time and then those.  Inside a block each warp takes 16 keys (32
 // of codes) of every tile through its own ring of cp.async stages: no barrier
 // until a piece ends.
 //
@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kMaxCtas = 512;                // counters and partial results in the workspace
 constexpr int kHeads = 8;                    // query heads of a unit
-constexpr int kFan = 16;                     // pieces that one warp joins, of one head
+constexpr int kFan = 16;                     // pieces that half a warp joins, of one head
 constexpr int kMinTile = 96;                 // keys of the smallest variant's tile
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
@@ -317,6 +317,11 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     __shared__ uint32_t sm_mask[W][S::kStages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int D = a.D;
+    // Work per head goes to half warps, so that eight heads take one turn (eight
+    // heads of one KV head, 5 requests of 4582 .. 9357 keys: 15.6 us, a warp a
+    // head 21.9 us; six heads alike): this lane's head there, and its place.
+    const int half_h = 2 * warp + (lane >> 4), half_lane = lane & 15;
+    static_assert(2 * W >= kHeads, "a half warp for each head");
 
     // rows without keys
     auto clear_rows = [&] {
@@ -430,9 +435,12 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         kpool = a.k + head * a.head_bytes + row0 * a.row_bytes + chunk * 16;
         // its queries are on their way to L1 while its keys are fetched
         const int skip = a.skip_of(load.u, head);
-        const float *row = a.q + load.r * a.ldq + (int64_t)(head * a.group + skip + warp) * D;
-        if (warp < min(kHeads, a.group - skip) && 4 * lane < D)
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(row + 4 * lane));
+        const float *row = a.q + load.r * a.ldq + (int64_t)(head * a.group + skip + half_h) * D;
+        if (half_h < min(kHeads, a.group - skip))
+#pragma unroll
+            for (int c = 8 * half_lane; c < DP; c += 128)
+                if (c < D)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(row + c));
     };
     // The next step's first key and, for every 16 keys of which some are
     // visible, their page (the short way: pages hold whole sixteens of keys),
@@ -558,32 +566,34 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         *reinterpret_cast<float4 *>(to + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     };
     auto put_sum = [&](const Unit &u, bool out, int piece, int h, float top, float sum_l) {
-        if (lane == 0) {
-            if (!out)
-                *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
-            else if (a.lse)
-                a.lse[(int64_t)u.r * a.heads + u.h0 + h] =
-                    sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
-        }
+        if (!out)
+            *reinterpret_cast<float2 *>(pc.at_ml(piece, h)) = make_float2(top, sum_l);
+        else if (a.lse)
+            a.lse[(int64_t)u.r * a.heads + u.h0 + h] = sum_l == 0.f ? -INFINITY : (top - kUp) * kLn2 + logf(sum_l);
     };
-    // Maximum and sum over the lanes' parts, and each part's factor.
-    auto over_parts = [&](float2 ml, float &f, float &top, float &sum_l) {
-        top = ml.x;
+    // Maximum and sum over the parts that a half warp's lanes hold, two each,
+    // and each part's factor.
+    auto over_parts = [&](const float2 (&ml)[2], float (&f)[2], float &top, float &sum_l) {
+        top = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
-        for (int x = 16; x; x >>= 1)
+        for (int x = 8; x; x >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-        sum_l = ml.y != ml.y ? ml.y : ml.y * f;   // (a NaN sum without a maximum stays one)
+        sum_l = 0.f;
 #pragma unroll
-        for (int x = 16; x; x >>= 1)
+        for (int k = 0; k < 2; ++k) {
+            f[k] = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - top);
+            sum_l += ml[k].y != ml[k].y ? ml[k].y : ml[k].y * f[k];   // (a NaN sum without a maximum stays one)
+        }
+#pragma unroll
+        for (int x = 8; x; x >>= 1)
             sum_l += __shfl_xor_sync(0xffffffffu, sum_l, x);
     };
+    const float2 no_part = make_float2(-INFINITY, 0.f);
     auto add = [](float4 &x, float4 y, float w) {
         x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y);
         x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
     };
-    constexpr int kQuads = DP > 128 ? 2 : 1;
-    const int c0 = min(4 * lane, DP - 4);   // this lane's columns, and those 128 on
+    constexpr int kQuads = DP / 64;   // a lane's fours of columns: 4 * half_lane + 64 * q
 
     // Queries as the MMA's B operand, in parts: [step][part][lane] the two
     // words that a lane feeds for head lane / 4 of the unit.
@@ -618,15 +628,13 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         if (fresh) {
             const int kv = a.kv_of(use.u), skip = a.skip_of(use.u, kv);
             const int h0 = kv * a.group + skip, heads = min(kHeads, a.group - skip);
-#pragma unroll 1
-            for (int h = warp; h < kHeads; h += W) {
+            if (const int h = half_h; h < kHeads) {   // (whole warps)
                 const float *row = a.q + use.r * a.ldq + (int64_t)(h0 + h) * D;
-                constexpr int kQuads = DP > 128 ? 2 : 1;
                 float x[kQuads][4];
                 float top = 0.f, poison = 0.f;   // poison: NaN if a query is, or is infinite
 #pragma unroll
                 for (int q = 0; q < kQuads; ++q) {
-                    const int c = 4 * lane + 128 * q;
+                    const int c = 4 * half_lane + 64 * q;
                     const float4 v = h < heads && c < D ? *reinterpret_cast<const float4 *>(row + c)
                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                     x[q][0] = v.x * a.mul, x[q][1] = v.y * a.mul, x[q][2] = v.z * a.mul, x[q][3] = v.w * a.mul;
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     // codes it is brought below 2^23 - 2^15, the most that three
                     // balanced digits of eight bits hold, and rounded there.
 #pragma unroll
-                    for (int s = 16; s; s >>= 1) {
+                    for (int s = 8; s; s >>= 1) {
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
                         poison += __shfl_xor_sync(0xffffffffu, poison, s);
                     }
@@ -651,13 +659,11 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     norm = some ? __uint_as_float((uint32_t)(127 + kAt - e) << 23) : 1.f;
                     back = (some ? __uint_as_float((uint32_t)(127 - kAt + e) << 23) : 1.f) + poison;
                 }
-                if (lane == 0)
+                if (half_lane == 0)
                     sm_back[h] = back;
 #pragma unroll
                 for (int q = 0; q < kQuads; ++q) {
-                    const int c = 4 * lane + 128 * q;   // columns c .. c + 3
-                    if (c >= DP)
-                        continue;
+                    const int c = 4 * half_lane + 64 * q;   // columns c .. c + 3
                     if constexpr (S::kCodes) {
                         uint32_t word[3] = {0, 0, 0};
 #pragma unroll
@@ -901,25 +907,32 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             const int mine_piece = 2 * (int)blockIdx.x + (ubeg >= begin ? 1 : 0);
             const Unit unit{use.r, h0, heads, ubeg, uend};
             __syncthreads();
-            // ---- the warps' parts, a head to a warp
-#pragma unroll 1
-            for (int h = warp; h < heads; h += W) {
-                float f, top, sum_l;
-                over_parts(lane < W ? make_float2(sm_m[lane % W][h], sm_l[lane % W][h])
-                                    : make_float2(-INFINITY, 0.f), f, top, sum_l);
+            // ---- the warps' parts
+            if (2 * warp < heads) {
+                const int h = min(half_h, heads - 1);   // (two halves of the last head write the same)
+                const float2 ml[2] = {half_lane < W ? make_float2(sm_m[half_lane % W][h], sm_l[half_lane % W][h])
+                                                    : no_part, no_part};
+                float f[2], top, sum_l;
+                over_parts(ml, f, top, sum_l);
                 const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+                float4 x[kQuads];
 #pragma unroll
-                for (int q = 0; q < kQuads; ++q) {
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int q = 0; q < kQuads; ++q)
+                    x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        add(x, *reinterpret_cast<const float4 *>(smem + (w * S::kStages + stage) * S::kStage +
-                                                                 at(h, c0 + 128 * q) * 4),
-                            __shfl_sync(0xffffffffu, f, w));
-                    if (4 * lane + 128 * q < D)
-                        put(unit, whole, mine_piece, h, 4 * lane + 128 * q, x, inv);
+                for (int w = 0; w < W; ++w) {
+                    const float fw = __shfl_sync(0xffffffffu, f[0], w, 16);
+                    const uint8_t *part_w = smem + (w * S::kStages + stage) * S::kStage;
+#pragma unroll
+                    for (int q = 0; q < kQuads; ++q)
+                        add(x[q], *reinterpret_cast<const float4 *>(part_w + at(h, 4 * half_lane + 64 * q) * 4), fw);
                 }
-                put_sum(unit, whole, mine_piece, h, top, sum_l);
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q)
+                    if (4 * half_lane + 64 * q < D)
+                        put(unit, whole, mine_piece, h, 4 * half_lane + 64 * q, x[q], inv);
+                if (half_lane == 0)
+                    put_sum(unit, whole, mine_piece, h, top, sum_l);
             }
             if (!whole)   // joined when the run is over: nothing in it waits for the counts
                 (ubeg >= begin ? after : before_it) = unit;
@@ -931,10 +944,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     }
     cp_async_wait<0>();
     __syncwarp();   // the warp's stages are its own again
-    float *mine = reinterpret_cast<float *>(smem + warp * S::kStages * S::kStage);
+    float *mine = reinterpret_cast<float *>(smem + (warp * S::kStages + (lane >> 4)) * S::kStage);
     // A unit's pieces: the second of the block with its first tile, the first
     // of the others.  kFan of them are joined into the first of them (into the
-    // output if there are no more), then those; each head by the warp that
+    // output if there are no more), then those; each head by the half warp that
     // counts to the last of them.
     struct Join {
         int b_first, b_last, b0, into, bunches;
@@ -957,18 +970,17 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             *ctr = 0;
         return is;
     };
-#pragma unroll 1
-    for (int h = warp; h < max(before_it.heads, after.heads); h += W) {
-        // lane 0 counts for the first piece, lane 1 for the second, at once
+    if (2 * warp < max(before_it.heads, after.heads)) {
+        const int h = half_h;
+        // lane 0 of a half counts for the first piece, lane 1 for the second, at once
         bool done = false;
-        if (lane < 2 && h < (lane ? after.heads : before_it.heads))
-            done = last_of(counters + (lane ? join_1.into : join_0.into) * kHeads + h,
-                           in_bunch(lane ? join_1 : join_0));
+        if (half_lane < 2 && h < (half_lane ? after.heads : before_it.heads))
+            done = last_of(counters + (half_lane ? join_1.into : join_0.into) * kHeads + h,
+                           in_bunch(half_lane ? join_1 : join_0));
         const uint32_t whose = __ballot_sync(0xffffffffu, done);
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
-            if (!((whose >> k) & 1))
-                continue;
+            bool mine_too = (whose >> ((lane & 16) + k)) & 1;   // this half joins
             const Unit unit = k ? after : before_it;
             const Join j = k ? join_1 : join_0;
 #pragma unroll 1
@@ -979,31 +991,37 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                 if (level) {
                     __syncwarp();
                     bool last = false;
-                    if (lane == 0)
+                    if (mine_too && half_lane == 0)
                         last = last_of(counters + (2 * kMaxCtas + j.b_first) * kHeads + h, count);
-                    if (!__shfl_sync(0xffffffffu, last, 0))
-                        break;
+                    mine_too = __shfl_sync(0xffffffffu, last, 0, 16);
                 }
-                __syncwarp();   // (what the count has seen, for every lane)
-                float f, top, sum_l;
-                // the pieces come through the warp's stage, every lane
-                // fetching the columns that it reads
-                const uint32_t dst = smem_u32(mine) + c0 * 4;
+                if (!__any_sync(0xffffffffu, mine_too))
+                    break;
+                __syncwarp();   // (what the counts have seen, for every lane)
+                // the pieces come through the half's stage, every lane fetching
+                // the columns that it reads
+                const uint32_t dst = smem_u32(mine) + 16 * half_lane;
                 auto fill = [&](int i) {
 #pragma unroll 4
                     for (int z = 0; z < kFan; ++z) {
-                        const bool some = i + z < count;
-                        const float *p = pc.at_o(piece_of(j, from + (some ? i + z : 0) * step), h) + c0;
+                        const bool some = mine_too && i + z < count;
+                        const float *p = pc.at_o(piece_of(j, from + (some ? i + z : 0) * step), h) + 4 * half_lane;
 #pragma unroll
                         for (int q = 0; q < kQuads; ++q)
-                            cp_async16(dst + (z * DP + 128 * q) * 4, p + 128 * q, some);
+                            cp_async16(dst + (z * DP + 64 * q) * 4, p + 64 * q, some);
                     }
                     commit();
                 };
                 fill(0);
-                over_parts(lane < count ? __ldcg(reinterpret_cast<const float2 *>(
-                                              pc.at_ml(piece_of(j, from + lane * step), h)))
-                                        : make_float2(-INFINITY, 0.f), f, top, sum_l);
+                float2 ml[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    ml[e] = mine_too && half_lane + 16 * e < count
+                                ? __ldcg(reinterpret_cast<const float2 *>(
+                                      pc.at_ml(piece_of(j, from + (half_lane + 16 * e) * step), h)))
+                                : no_part;
+                float f[2], top, sum_l;
+                over_parts(ml, f, top, sum_l);
                 float4 x[kQuads];
 #pragma unroll
                 for (int q = 0; q < kQuads; ++q)
@@ -1013,10 +1031,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     cp_async_wait<0>();
 #pragma unroll
                     for (int z = 0; z < kFan; ++z) {
-                        const float w = __shfl_sync(0xffffffffu, f, i + z);   // 0 past the last
+                        const float w = __shfl_sync(0xffffffffu, i ? f[1] : f[0], z, 16);   // 0 past the last
 #pragma unroll
                         for (int q = 0; q < kQuads; ++q)
-                            add(x[q], *reinterpret_cast<const float4 *>(mine + z * DP + c0 + 128 * q), w);
+                            add(x[q], *reinterpret_cast<const float4 *>(mine + z * DP + 4 * half_lane + 64 * q), w);
                     }
                     i += kFan;
                     if (i >= count)
@@ -1024,11 +1042,14 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                     fill(i);
                 }
                 const float inv = !out ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+                if (mine_too) {
 #pragma unroll
-                for (int q = 0; q < kQuads; ++q)
-                    if (4 * lane + 128 * q < D)
-                        put(unit, out, j.into, h, 4 * lane + 128 * q, x[q], inv);
-                put_sum(unit, out, j.into, h, top, sum_l);
+                    for (int q = 0; q < kQuads; ++q)
+                        if (4 * half_lane + 64 * q < D)
+                            put(unit, out, j.into, h, 4 * half_lane + 64 * q, x[q], inv);
+                    if (half_lane == 0)
+                        put_sum(unit, out, j.into, h, top, sum_l);
+                }
                 if (out)
                     break;
             }
@@ -1087,7 +1108,7 @@ cudaError_t launch(const PagedAttention &p, uint32_t *err, cudaStream_t stream)
     const int64_t tiles = p.requests * a.units * ceil_div(a.cap, S::kTile);
     int64_t grid = (int64_t)sms * S::kBlocks;
     grid = grid < kMaxCtas ? grid : kMaxCtas;
-    static_assert(kFan * 32 >= kMaxCtas && S::kWarps <= kFan, "a lane for each part");
+    static_assert(2 * kFan * kFan >= kMaxCtas && S::kWarps <= kFan, "two parts a lane of a half");
     grid = grid < tiles ? grid : tiles;
     kernel<<<(unsigned)grid, S::kThreads, S::kSmem, stream>>>(a);
     return cudaGetLastError();
