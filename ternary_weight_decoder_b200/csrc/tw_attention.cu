@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         if (i < 0)
             continue;
 
-        // ---- a new piece: its queries, a head to a warp, split
+        // ---- a new piece: its queries, split
         if (fresh) {
             const int kv = a.kv_of(use.u), skip = a.skip_of(use.u, kv);
             const int h0 = kv * a.group + skip, heads = min(kHeads, a.group - skip);

@@ -184,16 +184,14 @@ __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, flo
             a.xq[m * a.K + col(i)] = (int8_t)word;
     }
     if (a.qsum) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __reduce_add_sync(0xffffffffu, sum);
         if ((tid & 31) == 0)
             red_i[tid >> 5] = sum;
         __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < warps; ++w)
-                sum += red_i[w];
-            a.qsum[m] = sum;
+        if (tid < 32) {
+            sum = __reduce_add_sync(0xffffffffu, tid < warps ? red_i[tid] : 0);
+            if (tid == 0)
+                a.qsum[m] = sum;
         }
     }
     if (tid == 0)
