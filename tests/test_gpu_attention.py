@@ -407,3 +407,18 @@ def test_pools_with_strides_past_32_bits(dev, api):
     api.check()
     assert torch.equal(outs[0], outs[1]) and float(outs[0].abs().max()) > 0
     assert torch.equal(cache.k[1], dense.k[1]) and torch.equal(cache.v[0], dense.v[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("heads,hk,d", [(8, 1, 128), (7, 1, 64), (9, 1, 128), (15, 1, 64), (3, 1, 256), (8, 1, 256)])
+def test_attention_joins_of_every_head_count(dev, api, dtype, heads, hk, d):
+    """One to eight heads of a unit, in more pieces than one join takes."""
+    lengths = [14000, 5, 0, 3500]
+    cache, q, table = make(api, dev, dtype, lengths, heads, hk, d, 64, heads * d)
+    ws = api.paged_attention_workspace(len(lengths), heads, cache)
+    args = (G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev))
+    out, lse = api.paged_attention(*args, ws=ws, return_lse=True)
+    api.check()
+    check_all(api, cache, q, table, lengths, None, out, lse, heads)
+    o2, l2 = api.paged_attention(*args, ws=ws, return_lse=True)
+    assert bool((o2 == out).all()) and bool((l2 == lse).all())

@@ -185,3 +185,26 @@ def test_norm_on_another_stream(dev, api):
     got = [api.residual_norm(x, y, stream=s) for _ in range(10)]
     s.synchronize()
     assert all(torch.equal(g.n, want.n) and torch.equal(g.h, want.h) for g in got)
+
+
+@pytest.mark.parametrize("m,k", [(150, 1), (150, 256), (150, 171), (1800, 171), (1800, 256), (150, 301), (150, 513),
+                                 (150, 1025), (150, 1537), (150, 2049), (150, 2561), (150, 4097), (150, 6145),
+                                 (150, 8193), (150, 20001), (2, 1025), (2, 4097), (2, 8193), (150, 2052),
+                                 (150, 4100), (150, 6148), (150, 8196), (150, 10244), (150, 12292), (150, 16388),
+                                 (2, 4100), (2, 8196), (2, 16388)])
+def test_norm_and_codes_at_every_row_shape(dev, api, m, k):
+    """Widths on both sides of where threads and columns a thread change, for few rows and for many."""
+    c = _case(np.random.default_rng(m + k), m, k, "layer", "rms", "token")
+    r = _run(api, dev, c, "layer", "rms", -1.3, 1e-5)
+    codes = _run(api, dev, c, "layer", "rms", -1.3, 1e-5, quantize=True)
+    api.check()
+    h, n, dh, dn = _want(c, "layer", "rms", -1.3, 1e-5)
+    _close(r.h, h, dh)
+    _close(r.n, n, dn)
+    got = r.n.cpu().numpy()
+    amax = np.abs(got).max(axis=1)
+    assert np.array_equal(codes.amax.cpu().numpy(), amax)
+    scale = np.divide(np.float32(127), amax, out=np.zeros_like(amax), where=amax > 0)
+    want = np.clip(np.rint(got * scale[:, None]), -128, 127).astype(np.int8)
+    assert np.array_equal(codes.xq.cpu().numpy(), want)
+    assert np.array_equal(codes.qsum.cpu().numpy(), want.astype(np.int32).sum(axis=1))
