@@ -7,15 +7,19 @@
 // (u - mean(u)) / sqrt(var(u) + eps) * w + b.
 // The codes are those of tw_quantize_act on n, bit for bit.
 //
-// A row of x and y is read once and held in registers from then on; sums are
-// in 32 bits, the variance from the centred values.  Bound by memory, 16 bytes
-// per element (x, y in; h, n out): 4096 rows of 1536 with both norms and a
-// gate take 19.0 us (5.3 TB/s), of 8960 in 1000 rows 30.0 us (4.8 TB/s).
-// Measured and left out: persistent blocks with the next rows on their way
-// into shared memory (24.9 and 47.1 us: with one row at a time in a block the
-// reductions' latency shows), a warp a row (35.1 us at 1536).
+// A row is read once: y (or x alone) into registers, x and a gate per token
+// meanwhile into registers, shared memory or L2; sums are in 32 bits, the
+// variance from the centred values.  Bound by memory, 16 bytes per element (x,
+// y in; h, n out): 4096 rows of 1536 with both norms and a gate take 18.4 us
+// (5.5 TB/s), of 8960 in 1000 rows 27.5 us (5.2 TB/s); odd widths, column by
+// column, about 0.6 of that.  Measured and left out: persistent blocks with the
+// next rows on their way into shared memory (24.9 and 47.1 us: with one row at
+// a time in a block the reductions' latency shows), a warp a row (35.1 us at
+// 1536), odd widths in groups of four between memory's boundaries with their
+// ends apart (2492 rows of 2407: 33 us, single columns 26 us).
 #include "tw_device.cuh"
 #include "tw_internal.h"
+#include "tw_kv.cuh"
 
 namespace tw {
 namespace {
@@ -75,9 +79,9 @@ template <> struct Vec<1> {
 // norm, residual sum, norm and codes.  Thread t has columns
 // V * (t + i * STRIDE) + 0 .. V - 1 (STRIDE 0: blockDim); x_at(i, v) and gate_at(i, v) give x and
 // the gate there.
-template <int V, int PER, int STRIDE, class X, class G>
+template <int V, int PER, int STRIDE, class A, class X, class G>
 __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, float (&u)[PER][V], Reduction &sums,
-                                           int *red_i, X x_at, G gate_at)
+                                           int *red_i, A arrive, X x_at, G gate_at)
 {
     const int threads = STRIDE ? STRIDE : blockDim.x, tid = threadIdx.x, K = (int)a.K, warps = threads / 32;
     const float inv = 1.0f / (float)K;
@@ -136,6 +140,7 @@ __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, flo
 
     if (a.y) {
         norm(u, a.post, a.post_w, a.post_b);
+        arrive();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (col(i) >= K)
@@ -200,12 +205,19 @@ __device__ __forceinline__ void finish_row(const ResidualNorm &a, int64_t m, flo
 
 // Blocks that share an SM, so that one loads while another reduces: of 512
 // threads three where a thread has few columns (4096 rows of 1536: 19.0 us, two
-// 20.3 us), else two (1000 rows of 8960: 30.0 us; three would spill: 33.9 us).
+// 20.3 us), else two.
 template <int VALUES, int THREADS>
 constexpr int kBlocks = (VALUES <= 16 && THREADS <= 512 ? 1536 : 1024) / THREADS;
 
+// Where x waits while y is normed: shared memory leaves registers to the row
+// and so another block to the SM (1000 rows of 8960: three blocks 27.5 us, two
+// with x in registers 30.3 us).
+enum Wait { kL2, kRegisters, kShared };
+template <int VALUES, int THREADS, int BLOCKS>
+constexpr Wait kWait = VALUES <= 8 || (VALUES <= 20 && BLOCKS * THREADS <= 1024) ? kRegisters : kL2;
+
 // One block a row: of THREADS threads (STRIDE), or of as many as fill it.
-template <int V, int PER, int THREADS, int STRIDE, int BLOCKS>
+template <int V, int PER, int THREADS, int STRIDE, int BLOCKS, Wait WAIT>
 __global__ void __launch_bounds__(THREADS, BLOCKS) k_residual_norm(const ResidualNorm a)
 {
     __shared__ float red[2][32];
@@ -226,55 +238,106 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_residual_norm(const Residua
             }
         }
     };
-    // x is on its way while y is normed: into registers where they hold both,
-    // else into L2, as a gate per token
+    // x is on its way while y is normed, and a gate per token: into shared
+    // memory, where a thread finds what it fetched itself, or x into registers
+    // where they hold both, else into L2
+    extern __shared__ __align__(16) float staged[];
+    auto stage = [&](const float *row, float *to) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (col(i) >= K)
+                continue;
+            else if (V == 4)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + col(i))),
+                             "l"(row + col(i)) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + col(i))),
+                             "l"(row + col(i)) : "memory");
+    };
     auto ahead = [&](const float *row) {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (col(i) < K && (V > 1 || tid % 8 == 0))
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(row + col(i)));
     };
-    constexpr bool kAhead = V * PER <= 8 || (V * PER <= 20 && BLOCKS * THREADS <= 1024);
-    float u[PER][V], x[kAhead ? PER : 1][V];
+    const bool gate_row = a.gate && a.ldg;
+    float *const staged_gate = staged + K;
+    float u[PER][V], x[WAIT == kRegisters ? PER : 1][V];
     read((a.y ? a.y + m * a.ldy : a.x + m * a.ldx), u);
     if (a.y) {
-        if constexpr (kAhead)
+        if constexpr (WAIT == kRegisters)
             read(a.x + m * a.ldx, x);
+        else if constexpr (WAIT == kShared)
+            stage(a.x + m * a.ldx, staged);
         else
             ahead(a.x + m * a.ldx);
-        if (a.gate && a.ldg)
-            ahead(a.gate + m * a.ldg);
+        if (gate_row) {
+            if constexpr (WAIT == kShared)
+                stage(a.gate + m * a.ldg, staged_gate);
+            else
+                ahead(a.gate + m * a.ldg);
+        }
     }
     finish_row<V, PER, STRIDE>(
         a, m, u, sums, red_i,
+        [] {
+            if constexpr (WAIT == kShared)
+                asm volatile("cp.async.wait_all;" ::: "memory");
+        },
         [&](int i, float (&v)[V]) {
-            if constexpr (kAhead) {
+            if constexpr (WAIT == kRegisters) {
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     v[j] = x[i][j];
             } else {
-                Vec<V>::load(a.x + m * a.ldx + col(i), v);
+                Vec<V>::load((WAIT == kShared ? staged : a.x + m * a.ldx) + col(i), v);
             }
         },
-        [&](int i, float (&v)[V]) { Vec<V>::load(a.gate + m * a.ldg + col(i), v); });
+        [&](int i, float (&v)[V]) {
+            Vec<V>::load((WAIT == kShared && gate_row ? staged_gate : a.gate + m * a.ldg) + col(i), v);
+        });
 }
+
+constexpr int kSharedMost = 224 * 1024;   // of a block, beside its static shared memory
+
+// A row of x, and of a gate per token.
+int64_t shared_bytes(const ResidualNorm &a) { return (a.y ? a.gate && a.ldg ? 2 : 1 : 0) * a.K * (int64_t)sizeof(float); }
 
 template <int V, int PER, int THREADS = 512, int BLOCKS = kBlocks<V * PER, THREADS>>
 cudaError_t launch(const ResidualNorm &a, cudaStream_t stream)
 {
     // whole warps, PER groups a thread
     const int64_t groups = (a.K + V - 1) / V, threads = (groups + 32 * PER - 1) / (32 * PER) * 32;
-    k_residual_norm<V, PER, THREADS, 0, BLOCKS><<<(unsigned)a.M, (unsigned)threads, 0, stream>>>(a);
+    k_residual_norm<V, PER, THREADS, 0, BLOCKS, kWait<V * PER, THREADS, BLOCKS>>
+        <<<(unsigned)a.M, (unsigned)threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
 // Every thread of THREADS, its groups a constant apart: where they are many,
 // addresses and bounds of any other distance would not fit the registers (by
-// single columns 1280 rows of 4687: 32 us, 69 us).
+// single columns 1280 rows of 4687: 32 us, 69 us; quads from shared memory,
+// 1785 rows of 8960: 44.1 us, 51.2 us).
 template <int V, int PER, int THREADS, int BLOCKS = kBlocks<V * PER, THREADS>>
 cudaError_t launch_all(const ResidualNorm &a, cudaStream_t stream)
 {
-    k_residual_norm<V, PER, THREADS, THREADS, BLOCKS><<<(unsigned)a.M, THREADS, 0, stream>>>(a);
+    k_residual_norm<V, PER, THREADS, THREADS, BLOCKS, kWait<V * PER, THREADS, BLOCKS>>
+        <<<(unsigned)a.M, THREADS, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// x and a gate per token wait in shared memory (STRIDE as the kernel's).
+template <int V, int PER, int BLOCKS, int THREADS = 512, int STRIDE = 0>
+cudaError_t launch_shared(const ResidualNorm &a, cudaStream_t stream)
+{
+    auto *kernel = k_residual_norm<V, PER, THREADS, STRIDE, BLOCKS, kShared>;
+    cudaError_t e = ask_once([] {
+        return cudaFuncSetAttribute(k_residual_norm<V, PER, THREADS, STRIDE, BLOCKS, kShared>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+    });
+    if (e != cudaSuccess)
+        return e;
+    const int64_t groups = (a.K + V - 1) / V, threads = (groups + 32 * PER - 1) / (32 * PER) * 32;
+    kernel<<<(unsigned)a.M, STRIDE ? STRIDE : (unsigned)threads, (size_t)shared_bytes(a), stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -296,18 +359,24 @@ cudaError_t launch_quads(const ResidualNorm &a, cudaStream_t stream)
         if (groups <= 4096)
             return launch_all<4, 4, 1024>(a, stream);
     }
-    // as few groups a thread as 512 threads allow, two at least
+    // as few groups a thread as 512 threads allow, two at least; a row and its
+    // gate wait in L2 where an SM holds fewer of them than blocks
     switch ((groups + 511) / 512) {
-    case 1: case 2: return launch<4, 2>(a, stream);
-    case 3: return launch<4, 3>(a, stream);
-    case 4: return launch<4, 4>(a, stream);
-    case 5: return launch<4, 5>(a, stream);
-    case 6: return launch<4, 6>(a, stream);
-    case 7: case 8: return launch_all<4, 8, 512>(a, stream);
-    default: return launch_all<4, 8, 1024>(a, stream);
+    case 1: case 2: return launch_shared<4, 2, 3>(a, stream);
+    case 3: return launch_shared<4, 3, 3, 512, 512>(a, stream);
+    case 4: return launch_shared<4, 4, 3, 512, 512>(a, stream);
+    case 5: return launch_shared<4, 5, 3, 512, 512>(a, stream);
+    case 6: return launch_shared<4, 6, 2, 512, 512>(a, stream);
+    case 7: case 8:
+        return 2 * shared_bytes(a) <= kSharedMost ? launch_shared<4, 8, 2, 512, 512>(a, stream)
+                                                  : launch_all<4, 8, 512>(a, stream);
+    default:
+        return shared_bytes(a) <= kSharedMost ? launch_shared<4, 8, 1, 1024, 1024>(a, stream)
+                                              : launch_all<4, 8, 1024>(a, stream);
     }
 }
 
+// Odd widths and strides.
 cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
 {
     if (a.M < 148) {
@@ -337,7 +406,7 @@ cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
     if (a.K <= 4096)
         return launch_all<1, 8, 512>(a, stream);
     if (a.K <= 6144)
-        return launch_all<1, 12, 512, 2>(a, stream);
+        return launch_shared<1, 12, 3, 512, 512>(a, stream);
     if (a.K <= 8192)
         return launch_all<1, 16, 512, 2>(a, stream);
     return a.K <= 16384 ? launch_all<1, 16, 1024>(a, stream) : launch_all<1, 32, 1024>(a, stream);
