@@ -343,15 +343,16 @@ cudaError_t launch_shared(const ResidualNorm &a, cudaStream_t stream)
 
 bool by16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows too few for every SM get threads enough for one group of columns each,
-// for latency (one row of 1536: 2.1 us, with two groups a thread 2.4; of 16384
-// with four groups 6.7, with eight 9.8).
+// Rows too few for every SM, or narrow ones for it twice, get threads enough
+// for one group of columns each, for latency (one row of 1536: 2.1 us, with two
+// groups a thread 2.4; 296 rows 3.7, 3.95; one of 16384 with four groups 7.3,
+// with eight 8.7).
 cudaError_t launch_quads(const ResidualNorm &a, cudaStream_t stream)
 {
     const int64_t groups = a.K / 4;
+    if (groups <= 512 && a.M <= 2 * 148)
+        return launch<4, 1>(a, stream);
     if (a.M < 148) {
-        if (groups <= 512)
-            return launch<4, 1>(a, stream);
         if (groups <= 1024)
             return launch<4, 1, 1024>(a, stream);
         if (groups <= 2048)
@@ -379,9 +380,9 @@ cudaError_t launch_quads(const ResidualNorm &a, cudaStream_t stream)
 // Odd widths and strides.
 cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
 {
+    if (a.K <= 1024 && a.M <= 2 * 148)
+        return launch<1, 1, 1024>(a, stream);
     if (a.M < 148) {
-        if (a.K <= 1024)
-            return launch<1, 1, 1024>(a, stream);
         if (a.K <= 2048)
             return launch<1, 2, 1024>(a, stream);
         if (a.K <= 4096)
