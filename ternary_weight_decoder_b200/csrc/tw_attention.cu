@@ -16,7 +16,7 @@
 // output; the pieces of one that spans blocks go to the workspace and are
 // joined in a fixed order, each head by the half warp that finishes it last,
 // kFan pieces at a time and then those.  Inside a block each warp takes 16 keys (32
-// of codes) of every tile through its own ring of cp.async stages: no barrier
+// of short rows) of every tile through its own ring of cp.async stages: no barrier
 // until a piece ends.
 //
 // Matrix products: the 16 keys (or 16 columns of the values) are the rows of
@@ -79,9 +79,12 @@ struct Shape {
     static constexpr int kElem = kCodes ? 1 : 2;
     static constexpr int kRow = DP * kElem;            // bytes of a key
     static constexpr int kChunks = kRow / 16;
-    // Keys of a warp's step: twice 16 of codes, so that a step moves as many
-    // bytes and its fixed instructions count for as little as of 16 bits.
-    static constexpr int kHalves = kCodes ? 2 : 1;
+    // Keys of a warp's step: twice 16 where rows are short (codes, up to 64
+    // columns), so that its fixed instructions count for less.  14 heads over 2
+    // of 64 columns: 119 requests of 121 .. 231 keys 9.9 us (16 a step: 12.8),
+    // 14 of 11500 .. 73268 49.1 us (50.7); but 212 of 24 .. 32 over 8 heads
+    // 20.4 us (17.4), as fewer steps are on their way.
+    static constexpr int kHalves = kCodes || DP <= 64 ? 2 : 1;
     static constexpr int kKeys = 16 * kHalves;
     static constexpr uint32_t kAll = kHalves == 2 ? 0xffffffffu : 0xffffu;
     static constexpr int kPool = kKeys * kRow;         // bytes of a step's keys
@@ -466,14 +469,25 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         int64_t slot = -1;   // codes: this lane's key
         auto half = [&](int h, int page0, int in0) {
             const uint32_t rows = base + h * 16 * S::kRow;
+            // Sixteen keys of which none is taken: their weights are 0, and 0
+            // times what the stage holds has to be (codes are finite).  A whole
+            // step of these is passed over.
+            auto no_values = [&] {
+                if (!S::kCodes && H == 2)
+                    for (int i = 0; i < 16 / kRowsPer; ++i)
+                        cp_async16(ring + rows + place<S::kChunks>(row0 + kRowsPer * i, chunk) + S::kPool, a.k, false);
+            };
             if (a.short_way) {
                 // visible keys of the sixteen, from which to which
                 const int from = max(load.s.lo - next_j - 16 * h, 0), to = min(load.s.hi - next_j - 16 * h, 16);
-                if (from >= to)
-                    return;   // none: a whole step of these is passed over, half a one is masked below
+                if (from >= to) {
+                    no_values();
+                    return;
+                }
                 if ((uint32_t)page0 >= (uint32_t)a.pages) {
                     if (lane == 0)
                         atomicOr(a.err, EFLAG_BADDESC);
+                    no_values();
                     return;
                 }
                 const uint8_t *ks = kpool + (uint64_t)(uint32_t)page0 * (uint32_t)a.page_bytes +
