@@ -10,8 +10,8 @@
 // A row is read once: y (or x alone) into registers, x and a gate per token
 // meanwhile into registers, shared memory or L2; sums are in 32 bits, the
 // variance from the centred values.  Bound by memory, 16 bytes per element (x,
-// y in; h, n out): 4096 rows of 1536 with both norms and a gate take 18.4 us
-// (5.5 TB/s), of 8960 in 1000 rows 27.5 us (5.2 TB/s); odd widths, column by
+// y in; h, n out): 4096 rows of 1536 with both norms and a gate take 19.2 us
+// (5.2 TB/s), of 8960 in 1000 rows 30.0 us (4.8 TB/s); odd widths, column by
 // column, about 0.6 of that.  Measured and left out: persistent blocks with the
 // next rows on their way into shared memory (24.9 and 47.1 us: with one row at
 // a time in a block the reductions' latency shows), a warp a row (35.1 us at
@@ -58,8 +58,15 @@ struct Reduction {
     }
 };
 
+// V columns of fp32.  `once`: of a row that is read once, kept out of L1 for
+// the weights' sake.
 template <int V> struct Vec;
 template <> struct Vec<4> {
+    static __device__ __forceinline__ void once(const float *p, float (&v)[4])
+    {
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p) : "memory");
+    }
     static __device__ __forceinline__ void load(const float *p, float (&v)[4])
     {
         const float4 f = *reinterpret_cast<const float4 *>(p);
@@ -230,7 +237,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_residual_norm(const Residua
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (col(i) < K) {
-                Vec<V>::load(row + col(i), v[i]);
+                // 4096 rows of 1536 into buffers that L2 holds: 19.2 us, through
+                // L1 20.3 us (into others alike); wide rows lose by it
+                if constexpr (V == 4 && PER <= 2)
+                    Vec<V>::once(row + col(i), v[i]);
+                else
+                    Vec<V>::load(row + col(i), v[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j)

@@ -422,3 +422,19 @@ def test_attention_joins_of_every_head_count(dev, api, dtype, heads, hk, d):
     check_all(api, cache, q, table, lengths, None, out, lse, heads)
     o2, l2 = api.paged_attention(*args, ws=ws, return_lse=True)
     assert bool((o2 == out).all()) and bool((l2 == lse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("heads,hk,d,page", [(14, 2, 64, 16), (8, 8, 64, 48), (6, 2, 32, 32), (4, 4, 48, 5)])
+def test_attention_masks_in_short_rows(dev, api, dtype, heads, hk, d, page):
+    """Sixteens of keys of which none is visible beside others, what the masked places hold being NaN."""
+    rng = np.random.default_rng(d + page)
+    lengths = [int(n) for n in rng.integers(1, 900, 24)] + [16, 17, 32, 33, 48, 49]
+    first = [int(rng.integers(0, n)) for n in lengths]
+    first[:4] = [lengths[0], max(lengths[1] - 3, 0), 16, -1]
+    cache, q, table = make(api, dev, dtype, lengths, heads, hk, d, page, heads, first=first)
+    args = (G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev))
+    for _ in range(3):
+        out, lse = api.paged_attention(*args, first=i32(first, dev), return_lse=True)
+        api.check()
+        check_all(api, cache, q, table, lengths, first, out, lse, heads)
