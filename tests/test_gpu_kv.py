@@ -236,3 +236,30 @@ def test_assign_flags_pages_that_are_none(dev, api):
         with pytest.raises(api.TernaryError, match="TW_ERR_CORRUPT"):
             api.check()
         assert a.slots.tolist() == ([-1, 8, 14] if table[0][0] < 0 else [31, -1, 14])
+
+
+def test_outputs_are_tensors_of_their_own(dev, api):
+    """Under gradients, without them and in inference mode; no output is a view of another."""
+    import torch
+    x = torch.randn(3, 64, device=dev)
+    w = torch.rand(64, device=dev).requires_grad_()
+    seen = []
+    for mode in (torch.enable_grad, torch.no_grad, torch.inference_mode):
+        with mode():
+            lengths, table = i32([0, 15, 3], dev), i32([[-1, -1], [4, -1], [2, -1]], dev)
+            a = api.kv_assign(lengths, i32([2, 2, 1], dev), table, i32([1, 0, 3, 5], dev), i32([4], dev), 16, 6)
+            r = api.residual_norm(x, x, pre="rms", pre_weight=w)
+            api.check()
+            assert all(not t.requires_grad and t._base is None for t in (*a, r.h, r.n))
+            before = [t.clone() for t in a]
+            a.slots.add_(1)
+            a.lengths.zero_()
+            for t, b in zip(a[1:2] + a[3:], before[1:2] + before[3:]):
+                assert torch.equal(t, b)
+            seen.append((before, r.n.clone()))
+            if mode is torch.enable_grad:   # what autograd saves of an output stays usable
+                (r.n * w).sum().backward()
+                n64 = r.n.double()   # three summands: two roundings of at most their sizes' sum
+                assert ((w.grad - n64.sum(0)).abs() <= 2 * 2 ** -24 * n64.abs().sum(0)).all()
+    for before, n in seen[1:]:
+        assert torch.equal(n, seen[0][1]) and all(torch.equal(p, q) for p, q in zip(before, seen[0][0]))
