@@ -372,14 +372,19 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     // A run that would end within `near` tiles of a unit's edge ends there, for
     // this block and its neighbour alike: a few tiles more or less cost less
     // than another piece (256 requests on codes: 127.7 us, 128.4 us without;
-    // with up to half a run 174.8 us).
+    // with up to half a run 174.8 us).  Runs of one to four tiles (near = 0): one
+    // whose last tile alone, or whose first alone, is another unit's than the
+    // others leaves it to its neighbour, the last of two such ends only, so that
+    // each run keeps a tile (25 requests of 12 .. 4404 keys, 8 heads of 256 over
+    // one: 16.1 us, 18.5 us without; 64 of 200 .. 600, 12 over 2: 12.9, 14.5).
     const uint32_t near = min(split.each / 4, 3u);
+    const bool alone = split.each == 1 && split.more == 0;   // a tile a block
     if (begin < end) {
         const uint32_t mine = before * a.units, past = (before + sum) * a.units;
-        if (tid == 0 && (near == 0 || end == total))
+        if (tid == 0 && (alone || end == total))
             bounds[1] = end;
 #pragma unroll 1
-        for (int k = 0; k < (near ? 2 : 1); ++k) {
+        for (int k = 0; k < (alone ? 1 : 2); ++k) {
             const uint32_t at = k ? end : begin;
             if (at < mine || at >= past)
                 continue;
@@ -393,8 +398,13 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             }
             c.u = in / c.s.tiles, c.t = in % c.s.tiles;
             uint32_t to = at;
-            const bool down = 2 * c.t < c.s.tiles;
-            if (c.t && (down ? c.t : c.s.tiles - c.t) <= near) {
+            bool down = 2 * c.t < c.s.tiles, snap = (down ? c.t : c.s.tiles - c.t) <= near;
+            if (near == 0) {
+                const uint32_t edge = blockIdx.x + k;   // this run's begin or end, among all runs' (0: c.t is 0)
+                down = c.t == 1 && split.begin(edge - 1) + 1 < at;
+                snap = down || (c.t + 1 == c.s.tiles && split.begin(min(edge + 1, G)) >= at + 3);
+            }
+            if (c.t && snap) {
                 to = down ? at - c.t : at + c.s.tiles - c.t;
                 c.t = down ? 0 : c.s.tiles - 1;
                 if (!down) {
@@ -970,6 +980,13 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     auto join_of = [&](const Unit &u) {
         Join j;
         j.b_first = split.block_of(u.beg + near), j.b_last = split.block_of(u.end - near - 1);
+        if (near == 0) {   // a neighbour may have taken over their only tile of the unit
+            if (split.begin(j.b_last) + 1 == u.end && split.begin(j.b_last + 1) >= u.end + 2 &&
+                !(u.beg + 2 == u.end && split.begin(j.b_last - 1) < u.beg))
+                --j.b_last;
+            if (split.begin(j.b_first + 1) == u.beg + 1 && split.begin(j.b_first) < u.beg)
+                ++j.b_first;
+        }
         j.bunches = (j.b_last - j.b_first) / kFan + 1;
         j.b0 = j.b_first + ((int)blockIdx.x - j.b_first) / kFan * kFan;
         j.into = piece_of(j, j.b0);

@@ -438,3 +438,23 @@ def test_attention_masks_in_short_rows(dev, api, dtype, heads, hk, d, page):
         out, lse = api.paged_attention(*args, first=i32(first, dev), return_lse=True)
         api.check()
         check_all(api, cache, q, table, lengths, first, out, lse, heads)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_attention_runs_of_few_tiles(dev, api, seed):
+    """Lengths of a few tiles each, so many that blocks have one to five: ends of runs next to ends of requests."""
+    rng = np.random.default_rng(seed)
+    count, top = int(rng.integers(40, 260)), int(rng.choice([150, 250, 400, 700, 1500]))
+    lengths = [int(n) for n in rng.integers(1, top, count)]
+    lengths[::17] = [0] * len(lengths[::17])
+    heads, hk, d = [(8, 1, 64), (4, 2, 128), (2, 1, 256)][seed % 3]
+    dtype = ["f16", "i8", "bf16"][seed // 3 % 3]
+    cache, q, table = make(api, dev, dtype, lengths, heads, hk, d, 32, seed, poison=False)
+    ws = api.paged_attention_workspace(count, heads, cache)
+    args = (G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev))
+    out, lse = api.paged_attention(*args, ws=ws, return_lse=True)
+    api.check()
+    check_all(api, cache, q, table, lengths, None, out, lse, heads)
+    o2, l2 = api.paged_attention(*args, ws=ws, return_lse=True)
+    assert bool((o2 == out).all()) and bool((l2 == lse).all())
+    assert not bool(ws[:3 * 512 * 8 * 4].any())   # the counters are zero between calls
