@@ -599,9 +599,11 @@ TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads
  * carried with at least 21 significant bits (cache elements exactly), but
  * queries to no less than 2^-23 of their head's largest and, on TW_KV_F16 and
  * TW_KV_I8, weights (times their value's scale) to no less than 2^-37 of the
- * largest.
+ * largest (or 2^-117 of the sum of weights, where that is more).
  * TW_KV_I8: the scales of visible keys and values are 0 or in
- * [2^-60, 2^60].  heads: a multiple of kv_heads.
+ * [2^-60, 2^60]; where keys whose value has a scale of 0 outweigh the others'
+ * weights times scales by 2^80, lse is off by up to 2^-16.
+ * heads: a multiple of kv_heads.
  */
 TW_API int tw_paged_attention(const float *q, int64_t ldq, int64_t requests, int64_t heads,
                               const tw_kv_cache *cache, const int32_t *block_table,
