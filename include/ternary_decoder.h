@@ -592,8 +592,13 @@ TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads
  *   out_i = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m);  lse_i = m + log sum_j e^(s_j - m)
  * A request that sees no key gets out = 0 and lse = -inf.  out has row stride
  * ldo; lse [requests x heads] may be NULL.  Nothing outside the visible keys
- * is used, whatever its pages hold; a visible NaN or infinity makes the
- * outputs that it enters NaN or infinite.  A length past max_pages * page_size and
+ * is used, whatever its pages hold.  Visible infinities and NaN (an fp16 cache
+ * holds infinities for what is past its range) give what the formula gives in
+ * fp32: an infinite value in its column, NaN beside one of the other sign or
+ * where its weight is below fp32's range; no weight for a score of -inf (a
+ * head with no other score: 0 and -inf); NaN for a score of +inf.  Pieces of
+ * requests that hold some are computed twice, the second time slowly.
+ * A length past max_pages * page_size and
  * a page outside the pools record TW_ERR_CORRUPT: the keys concerned are left
  * out.  Sums and softmax statistics are fp32; the products' operands are
  * carried with at least 21 significant bits (cache elements exactly), but

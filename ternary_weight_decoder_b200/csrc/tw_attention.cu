@@ -99,6 +99,12 @@ struct Shape {
     static constexpr int kSteps = DP / 16;             // 16 columns of values each
     static constexpr int kQueryParts = kBf || kCodes ? 3 : 2;
     static constexpr int kQuerySteps = kCodes ? DP / 32 : DP / 16;   // MMA steps over a key
+    // The running maximum is raised once a score passes it by this much (in
+    // powers of two), so that most steps leave the sums alone.  Weights are
+    // then up to 2^slack; fp16 ones are carried times 2^12 (as is the sum),
+    // so that the second part of small ones stays clear of fp16's smallest
+    // number and large ones below its largest.
+    static constexpr float kSlack = kBf ? 8.f : 3.f, kUp = kBf ? 0.f : 12.f;
     // Two blocks of six warps on an SM: while one ends a piece (a few thousand
     // cycles of latencies) the other streams.  256 requests of 512 .. 16384
     // keys of codes: 129 us, against 143 us with one block of twelve; 512 of
@@ -219,6 +225,17 @@ __device__ __forceinline__ uint32_t place(int row, int c)
     return (uint32_t)(row * CHUNKS + (c ^ row_swap<CHUNKS>(row))) * 16;
 }
 
+// Element c of a row of the cache.
+template <int DT>
+__device__ __forceinline__ float element(const uint8_t *row, int c)
+{
+    if (DT == TW_KV_I8)
+        return reinterpret_cast<const int8_t *>(row)[c];
+    if (DT == TW_KV_BF16)
+        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[c]);
+    return __half2float(reinterpret_cast<const __half *>(row)[c]);
+}
+
 // The visible keys of a request, as tiles.
 struct Span {
     int lo, hi, first_tile, tiles;
@@ -305,6 +322,88 @@ struct Split {
     }
 };
 
+// A warp's keys of one piece, for it to sum in whole fp32 numbers.
+struct Whole {
+    Span s;
+    int r, kv, h0, heads;        // request, KV head, first query head, query heads
+    int tile, last;              // from which tile to which
+};
+
+// Where a warp's stage holds column c of head h: permuted by the head against
+// bank conflicts.
+template <int DP>
+__device__ __forceinline__ int sum_at(int h, int c)
+{
+    return h * DP + (c ^ ((h >> 1) << 3));
+}
+
+// The maxima, sums of weights (2^up-fold) and sums of values of a piece's keys,
+// head by head, with nothing carried in parts.
+template <int DT, int DP>
+__device__ __forceinline__ void whole_numbers(const Args &a, const Whole &u, float *sums, float *maxima, float *weights)
+{
+    using S = Shape<DT, DP>;
+    constexpr int kCols = DP / 32, kTogether = DP > 128 ? 2 : 4;   // (keys)
+    constexpr float kUp = S::kUp;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = kCols * lane, D = a.D;   // this lane's columns, and queries
+    const int32_t *table = a.table + u.r * a.table_stride;
+#pragma unroll 1
+    for (int h = 0; h < u.heads; ++h) {
+        const float *row = a.q + u.r * a.ldq + (int64_t)(u.h0 + h) * D;
+        float q[kCols], x[kCols], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e)
+            q[e] = c0 + e < D ? row[c0 + e] * a.mul : 0.f, x[e] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < (u.last + 1 - u.tile) * S::kKeys && l == l; i += kTogether) {   // (NaN: so is all else)
+            const int j0 = (u.tile + i / S::kKeys) * S::kTile + warp * S::kKeys + i % S::kKeys;
+            const uint8_t *at_k[kTogether];
+            float score[kTogether], v_scale[kTogether];
+            bool some[kTogether];
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k) {
+                const int j = j0 + k, p = max(j, 0) / a.P, in = j - p * a.P;
+                const int page = j >= u.s.lo && j < u.s.hi ? __ldg(table + p) : -1;
+                some[k] = (uint32_t)page < (uint32_t)a.pages;
+                at_k[k] = a.k + u.kv * a.head_bytes + (some[k] ? page * a.page_bytes + in * a.row_bytes : 0);
+                float k_scale = 1.f;
+                v_scale[k] = 1.f;
+                if (S::kCodes) {
+                    const int64_t at = (some[k] ? (int64_t)page * a.P + in : 0) * a.kv_heads + u.kv;
+                    k_scale = a.k_scale[at], v_scale[k] = a.v_scale[at];
+                }
+                score[k] = 0.f;
+#pragma unroll
+                for (int e = 0; e < kCols; ++e)
+                    if (some[k] && c0 + e < D)
+                        score[k] = fmaf(q[e], element<DT>(at_k[k], c0 + e), score[k]);
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    score[k] += __shfl_xor_sync(0xffffffffu, score[k], o);
+                score[k] *= k_scale;
+            }
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k) {
+                if (!some[k])
+                    continue;
+                const float top = fmaxf(m, score[k]), f = top == m ? 1.f : ex2(m - top);
+                const float w = ex2(score[k] - (top == -INFINITY ? 0.f : top) + kUp);
+                m = top, l = fmaf(l, f, w);
+#pragma unroll
+                for (int e = 0; e < kCols; ++e)
+                    if (c0 + e < D)
+                        x[e] = fmaf(x[e], f, w * v_scale[k] * element<DT>(at_k[k] + a.v_of_k, c0 + e));
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kCols; ++e)
+            sums[sum_at<DP>(h, c0 + e)] = x[e];
+        if (lane == 0)
+            maxima[h] = m, weights[h] = l;
+    }
+}
+
 template <int DT, int DP>
 __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlocks)
     k_paged_attention(const Args a)
@@ -312,12 +411,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     using S = Shape<DT, DP>;
     constexpr bool BF = S::kBf;
     constexpr int W = S::kWarps, H = S::kHalves, kThreads = S::kThreads, kTile = S::kTile;
-    // The running maximum is raised once a score passes it by this much (in
-    // powers of two), so that most steps leave the sums alone.  Weights are
-    // then up to 2^slack; fp16 ones are carried times 2^12 (as is the sum),
-    // so that the second part of small ones stays clear of fp16's smallest
-    // number and large ones below its largest.
-    constexpr float kSlack = BF ? 8.f : 3.f, kUp = BF ? 0.f : 12.f;
+    constexpr float kSlack = S::kSlack, kUp = S::kUp;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t part[W];
     __shared__ int start[3];
@@ -624,6 +718,38 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
         x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
     };
     constexpr int kQuads = DP / 64;   // a lane's fours of columns: 4 * half_lane + 64 * q
+    // The warps' parts, in stage `at_stage` of each.
+    float odd = 0.f;   // NaN once a sum was, or was infinite
+    auto join_warps = [&](const Unit &u, bool whole, int piece, int at_stage) {
+        if (2 * warp >= u.heads)
+            return;
+        const int h = min(half_h, u.heads - 1);   // (two halves of the last head write the same)
+        const float2 ml[2] = {half_lane < W ? make_float2(sm_m[half_lane % W][h], sm_l[half_lane % W][h]) : no_part,
+                              no_part};
+        float f[2], top, sum_l;
+        over_parts(ml, f, top, sum_l);
+        const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
+        float4 x[kQuads];
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+            x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float fw = __shfl_sync(0xffffffffu, f[0], w, 16);
+            const uint8_t *part_w = smem + (w * S::kStages + at_stage) * S::kStage;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+                add(x[q], *reinterpret_cast<const float4 *>(part_w + sum_at<DP>(h, 4 * half_lane + 64 * q) * 4), fw);
+        }
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+            odd = fmaf(x[q].x, 0.f, fmaf(x[q].y, 0.f, fmaf(x[q].z, 0.f, fmaf(x[q].w, 0.f, odd))));
+            if (4 * half_lane + 64 * q < D)
+                put(u, whole, piece, h, 4 * half_lane + 64 * q, x[q], inv);
+        }
+        if (half_lane == 0)
+            put_sum(u, whole, piece, h, top, sum_l);
+    };
 
     // Queries as the MMA's B operand, in parts: [step][part][lane] the two
     // words that a lane feeds for head lane / 4 of the unit.
@@ -632,7 +758,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     float m[2], l[2], unscale[2];    // of heads 2 t4, 2 t4 + 1
     const int n = (int)(end - begin);
     int stage = 0;
-    bool fresh = true;
+    bool fresh = true, any_odd = false;
     enter_unit();
     look_up();
 #pragma unroll 1
@@ -913,8 +1039,6 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             const int h0 = kv * a.group + skip, heads = min(kHeads, a.group - skip);
             __syncwarp();   // the stage is read: it takes the warp's sums
             float *mine = reinterpret_cast<float *>(smem + (warp * S::kStages + stage) * S::kStage);
-            // [head][column], columns permuted by the head against bank conflicts
-            auto at = [](int h, int c) { return h * DP + (c ^ ((h >> 1) << 3)); };
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -925,11 +1049,11 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
 #pragma unroll
                 for (int c = 0; c < S::kSteps; ++c) {
                     if (S::kCodes) {
-                        *reinterpret_cast<float2 *>(mine + at(2 * t4 + h, 16 * c + 2 * g)) =
+                        *reinterpret_cast<float2 *>(mine + sum_at<DP>(2 * t4 + h, 16 * c + 2 * g)) =
                             make_float2(o[c][h], o[c][2 + h]);
                     } else {
-                        mine[at(2 * t4 + h, 16 * c + g)] = o[c][h];
-                        mine[at(2 * t4 + h, 16 * c + g + 8)] = o[c][2 + h];
+                        mine[sum_at<DP>(2 * t4 + h, 16 * c + g)] = o[c][h];
+                        mine[sum_at<DP>(2 * t4 + h, 16 * c + g + 8)] = o[c][2 + h];
                     }
                 }
             }
@@ -937,36 +1061,10 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
             const int mine_piece = 2 * (int)blockIdx.x + (ubeg >= begin ? 1 : 0);
             const Unit unit{use.r, h0, heads, ubeg, uend};
             __syncthreads();
-            // ---- the warps' parts
-            if (2 * warp < heads) {
-                const int h = min(half_h, heads - 1);   // (two halves of the last head write the same)
-                const float2 ml[2] = {half_lane < W ? make_float2(sm_m[half_lane % W][h], sm_l[half_lane % W][h])
-                                                    : no_part, no_part};
-                float f[2], top, sum_l;
-                over_parts(ml, f, top, sum_l);
-                const float inv = !whole ? 1.f : sum_l == 0.f ? 0.f : 1.f / sum_l;
-                float4 x[kQuads];
-#pragma unroll
-                for (int q = 0; q < kQuads; ++q)
-                    x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float fw = __shfl_sync(0xffffffffu, f[0], w, 16);
-                    const uint8_t *part_w = smem + (w * S::kStages + stage) * S::kStage;
-#pragma unroll
-                    for (int q = 0; q < kQuads; ++q)
-                        add(x[q], *reinterpret_cast<const float4 *>(part_w + at(h, 4 * half_lane + 64 * q) * 4), fw);
-                }
-#pragma unroll
-                for (int q = 0; q < kQuads; ++q)
-                    if (4 * half_lane + 64 * q < D)
-                        put(unit, whole, mine_piece, h, 4 * half_lane + 64 * q, x[q], inv);
-                if (half_lane == 0)
-                    put_sum(unit, whole, mine_piece, h, top, sum_l);
-            }
+            join_warps(unit, whole, mine_piece, stage);
             if (!whole)   // joined when the run is over: nothing in it waits for the counts
                 (ubeg >= begin ? after : before_it) = unit;
-            __syncthreads();   // the stages and sums are read
+            any_odd = __syncthreads_or(odd != odd);   // the stages and sums are read
             fresh = true;
         }
         use.next(a);
@@ -974,6 +1072,43 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
     }
     cp_async_wait<0>();
     __syncwarp();   // the warp's stages are its own again
+
+    // ---- infinities.  One times the parts of a weight or a query, of which one
+    // may be 0 or of the other sign, becomes NaN above: where a sum was not
+    // finite, its piece comes again from whole fp32 numbers, into the same place.
+    // (Looking for such sums costs 0.1 us of one short request's 8.3 us and 0.6 us
+    // of 256 requests' 126.7 on codes; each warp among its own sums 3.5 us of them.)
+    if (any_odd) {   // (by any thread, at the last piece's end)
+        Cursor<kTile> c;
+        c.r = start[0], c.u = start[1], c.t = start[2];
+        c.s = span_of<kTile>(a, c.r);
+        c.ahead(a);
+#pragma unroll 1
+        for (int left = n; left > 0;) {
+            const int kv = a.kv_of(c.u), skip = a.skip_of(c.u, kv), tiles = min(c.s.tiles - c.t, left);
+            const bool whole = c.t == 0 && tiles == c.s.tiles;
+            const int piece = 2 * (int)blockIdx.x + (c.t == 0 ? 1 : 0);
+            const Unit unit{c.r, kv * a.group + skip, min(kHeads, a.group - skip), 0, 0};
+            bool again = false;
+            for (int i = tid; i < unit.heads * D; i += kThreads) {
+                const int h = i / D, col = i - h * D;
+                const float x = whole ? a.out[unit.r * a.ldo + (int64_t)unit.h0 * D + i] : pc.at_o(piece, h)[col];
+                again = again || !(fabsf(x) <= FLT_MAX);
+            }
+            if (__syncthreads_or(again)) {
+                whole_numbers<DT, DP>(a, Whole{c.s, c.r, kv, unit.h0, unit.heads, c.s.first_tile + c.t,
+                                               c.s.first_tile + c.t + tiles - 1},
+                                      reinterpret_cast<float *>(smem + warp * S::kStages * S::kStage), sm_m[warp],
+                                      sm_l[warp]);
+                __syncthreads();
+                join_warps(unit, whole, piece, 0);
+                __syncthreads();
+            }
+            left -= tiles;
+            c.t += tiles - 1;
+            c.next(a);
+        }
+    }
     float *mine = reinterpret_cast<float *>(smem + (warp * S::kStages + (lane >> 4)) * S::kStage);
     // A unit's pieces: the second of the block with its first tile, the first
     // of the others.  kFan of them are joined into the first of them (into the
