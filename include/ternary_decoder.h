@@ -661,8 +661,9 @@ TW_API int tw_residual_norm(const tw_residual_norm_args *args, tw_stream_t strea
  *   x = x + down(SiLU(gate(h1)) * up(h1))
  * and behind the last layer h = rms(x) * norm_out.  The tables are those of
  * tw_chain_layer, with q's y = q and k's y = k.  M requests; positions, slots
- * and lengths as tw_kv_assign writes them for one new token each.  Every
- * table is checked before anything is launched.
+ * and lengths as tw_kv_assign writes them for one new token each.  hidden is
+ * at most 32768, as the norms' K.  Every table is checked before anything is
+ * launched.
  */
 typedef struct tw_cached_layer {
     tw_kv_cache cache;                    /* kv_heads * head_dim = kv_dim     */

@@ -1030,6 +1030,9 @@ int tw_decoder_chain_cached(const tw_chain_layer *layers, const tw_cached_layer 
     if (int rc = check_chain_buffers(buf))
         return rc;
     const tw_chain_buffers &b = *buf;
+    if (b.hidden > tw::kNormMaxK)
+        return fail(TW_ERR_SHAPE, "%s: hidden %lld above the norms' %lld columns", who,
+                    (long long)b.hidden, (long long)tw::kNormMaxK);
     if (!c || !c->x || !c->q || !c->k)
         return fail(TW_ERR_NULL, "%s: residual stream, q and k buffers required", who);
     if (!aligned16(c->x) || !aligned16(c->q) || !aligned16(c->k))

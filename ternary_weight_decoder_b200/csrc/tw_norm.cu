@@ -429,6 +429,8 @@ cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
 
 cudaError_t launch_residual_norm(const ResidualNorm &a, cudaStream_t stream)
 {
+    if (a.K < 1 || a.K > kNormMaxK)   // columns past the widest block's would be left out
+        return cudaErrorInvalidValue;
     // Groups of four columns where every row of every operand starts on a
     // 16-byte boundary, single columns elsewhere (odd widths, odd strides).
     const bool quads = a.K % 4 == 0 && a.ldx % 4 == 0 && a.ldy % 4 == 0 && a.ldg % 4 == 0 &&
