@@ -561,8 +561,10 @@ TW_API int tw_kv_assign(const int32_t *lengths, const int32_t *delta, int64_t re
  * angles positions[t] * inv_freq[i], i < rotary / 2 (fp64, formed and reduced
  * in fp64), the pair i being columns (i, i + rotary/2), or (2i, 2i + 1) when
  * interleaved:  (a, b) -> (a cos - b sin, b cos + a sin) in fp32.  q_out
- * (row stride ldqo; may be q with the same stride) receives every row's
- * queries.  Keys and values of a row with slots[t] < 0 are not written; a
+ * (row stride ldqo; may be q with the same stride, else shares no byte with
+ * q's, k's or v's rows, which may be columns of one buffer with it, nor with the
+ * cache, positions, slots or inv_freq) receives every row's queries.
+ * Keys and values of a row with slots[t] < 0 are not written; a
  * slot at or past the end of the pools records TW_ERR_CORRUPT and is not
  * written either.  Slots of different rows must differ.  TW_KV_I8: amax =
  * max |x| over the head, code = clamp(rint(x * (127.0f / amax)), -127, 127),

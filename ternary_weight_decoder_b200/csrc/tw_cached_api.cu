@@ -36,6 +36,28 @@ bool overlap(const void *a, int64_t an, const void *b, int64_t bn)
     return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
+// Whether n rows of aw bytes, al bytes apart, and n of bw, bl apart, share a byte
+// (al >= aw, bl >= bw: rows of one buffer side by side do not).
+bool rows_overlap(const void *a, int64_t al, int64_t aw, const void *b, int64_t bl, int64_t bw, int64_t n)
+{
+    if (!overlap(a, (n - 1) * al + aw, b, (n - 1) * bl + bw))
+        return false;
+    const int64_t to_b = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    // Row i of a and the first of b that ends behind its beginning: j * bl > i * al - to_b - bw
+    auto hit = [&](int64_t i, int64_t first) {
+        const int64_t after = i * al - to_b - bw;
+        const int64_t q = after / bl, j = (after < 0 && after % bl ? q - 1 : q) + 1;   // (the quotient's floor, plus one)
+        const int64_t row = j < first ? first : j;
+        return row <= first + n - 1 && row * bl < i * al - to_b + aw;
+    };
+    if (al == bl)   // row 0 of a against every distance between two rows
+        return hit(0, -(n - 1)) || hit(0, 0);
+    for (int64_t i = 0; i < n; ++i)
+        if (hit(i, 0))
+            return true;
+    return false;
+}
+
 int check_cache(const tw_kv_cache *c, const char *who)
 {
     if (!c || !c->k || !c->v)
@@ -92,6 +114,25 @@ int check_append(const tw::RopeAppend &r, const char *who)
         return fail(TW_ERR_SHAPE, "%s: rotary %d is not a multiple of 8 up to head_dim", who, r.rotary);
     if (r.q_out == r.q && r.ldqo != r.ldq)
         return fail(TW_ERR_SHAPE, "%s: q_out is q with another row stride", who);
+    // Rows are rotated in no order: what one writes none may read, but its own.
+    const struct { const float *p; int64_t ld, width; const char *name; } in[] = {
+        {r.q_out == r.q ? nullptr : r.q, r.ldq, q, "q"}, {r.k, r.ldk, wide, "k"}, {r.v, r.ldv, wide, "v"}};
+    for (const auto &i : in)
+        if (rows_overlap(r.q_out, 4 * r.ldqo, 4 * q, i.p, 4 * i.ld, 4 * i.width, r.rows))
+            return fail(TW_ERR_SHAPE, "%s: q_out overlaps %s", who, i.name);
+    const tw_kv_cache &c = r.cache;
+    const __int128 last = (__int128)(c.num_pages - 1) * c.page_stride + (__int128)(c.page_size - 1) * c.token_stride +
+                          (__int128)(c.kv_heads - 1) * c.head_stride + c.head_dim;
+    const int64_t pool = (int64_t)(last < INT64_MAX / 4 ? last : INT64_MAX / 4) * (c.dtype == TW_KV_I8 ? 1 : 2);
+    const int64_t scales = 4 * c.num_pages * c.page_size * c.kv_heads, bytes = 4 * ((r.rows - 1) * r.ldqo + q);
+    const struct { const void *p; int64_t bytes; const char *name; } other[] = {
+        {c.k, pool, "the key pool"}, {c.v, pool, "the value pool"},
+        {c.k_scale, scales, "the key scales"}, {c.v_scale, scales, "the value scales"},
+        {r.positions, 4 * r.rows, "positions"}, {r.slots, 4 * r.rows, "slots"},
+        {r.rotary ? r.inv_freq : nullptr, 4 * r.rotary, "inv_freq"}};
+    for (const auto &o : other)
+        if (overlap(r.q_out, bytes, o.p, o.bytes))
+            return fail(TW_ERR_SHAPE, "%s: q_out overlaps %s", who, o.name);
     return TW_OK;
 }
 
