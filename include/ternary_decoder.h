@@ -593,7 +593,8 @@ TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads
  *   s_j = scale * (q_i . k_j);  m = max s_j
  *   out_i = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m);  lse_i = m + log sum_j e^(s_j - m)
  * A request that sees no key gets out = 0 and lse = -inf.  out has row stride
- * ldo; lse [requests x heads] may be NULL.  Nothing outside the visible keys
+ * ldo; lse [requests x heads] may be NULL; out, lse and the workspace share no
+ * byte with one another, the cache or an input.  Nothing outside the visible keys
  * is used, whatever its pages hold.  Visible infinities and NaN (an fp16 cache
  * holds infinities for what is past its range) give what the formula gives in
  * fp32: an infinite value in its column, NaN beside one of the other sign or

@@ -86,6 +86,32 @@ int check_cache(const tw_kv_cache *c, const char *who)
     return TW_OK;
 }
 
+struct Bytes {
+    const void *p;
+    int64_t n;
+    const char *name;
+};
+
+// An output beside n operands (null: none).
+int apart(const Bytes &out, const Bytes *in, int n, const char *who)
+{
+    for (int i = 0; i < n; ++i)
+        if (overlap(out.p, out.n, in[i].p, in[i].n))
+            return fail(TW_ERR_SHAPE, "%s: %s overlaps %s", who, out.name, in[i].name);
+    return TW_OK;
+}
+
+int apart_from_cache(const Bytes &out, const tw_kv_cache &c, const char *who)
+{
+    const __int128 last = (__int128)(c.num_pages - 1) * c.page_stride + (__int128)(c.page_size - 1) * c.token_stride +
+                          (__int128)(c.kv_heads - 1) * c.head_stride + c.head_dim;
+    const int64_t pool = (int64_t)(last < INT64_MAX / 4 ? last : INT64_MAX / 4) * (c.dtype == TW_KV_I8 ? 1 : 2);
+    const int64_t scales = 4 * c.num_pages * c.page_size * c.kv_heads;
+    const Bytes in[] = {{c.k, pool, "the key pool"}, {c.v, pool, "the value pool"},
+                        {c.k_scale, scales, "the key scales"}, {c.v_scale, scales, "the value scales"}};
+    return apart(out, in, 4, who);
+}
+
 int check_rows(const float *p, int64_t ld, int64_t width, const char *who, const char *name)
 {
     if (!p)
@@ -120,20 +146,12 @@ int check_append(const tw::RopeAppend &r, const char *who)
     for (const auto &i : in)
         if (rows_overlap(r.q_out, 4 * r.ldqo, 4 * q, i.p, 4 * i.ld, 4 * i.width, r.rows))
             return fail(TW_ERR_SHAPE, "%s: q_out overlaps %s", who, i.name);
-    const tw_kv_cache &c = r.cache;
-    const __int128 last = (__int128)(c.num_pages - 1) * c.page_stride + (__int128)(c.page_size - 1) * c.token_stride +
-                          (__int128)(c.kv_heads - 1) * c.head_stride + c.head_dim;
-    const int64_t pool = (int64_t)(last < INT64_MAX / 4 ? last : INT64_MAX / 4) * (c.dtype == TW_KV_I8 ? 1 : 2);
-    const int64_t scales = 4 * c.num_pages * c.page_size * c.kv_heads, bytes = 4 * ((r.rows - 1) * r.ldqo + q);
-    const struct { const void *p; int64_t bytes; const char *name; } other[] = {
-        {c.k, pool, "the key pool"}, {c.v, pool, "the value pool"},
-        {c.k_scale, scales, "the key scales"}, {c.v_scale, scales, "the value scales"},
-        {r.positions, 4 * r.rows, "positions"}, {r.slots, 4 * r.rows, "slots"},
-        {r.rotary ? r.inv_freq : nullptr, 4 * r.rotary, "inv_freq"}};
-    for (const auto &o : other)
-        if (overlap(r.q_out, bytes, o.p, o.bytes))
-            return fail(TW_ERR_SHAPE, "%s: q_out overlaps %s", who, o.name);
-    return TW_OK;
+    const Bytes other[] = {{r.positions, 4 * r.rows, "positions"}, {r.slots, 4 * r.rows, "slots"},
+                           {r.rotary ? r.inv_freq : nullptr, 4 * r.rotary, "inv_freq"}};
+    const Bytes out{r.q_out, 4 * ((r.rows - 1) * r.ldqo + q), "q_out"};
+    if (int rc = apart_from_cache(out, r.cache, who))
+        return rc;
+    return apart(out, other, 3, who);
 }
 
 int check_attention(const tw::PagedAttention &p, size_t ws_bytes, const char *who)
@@ -164,6 +182,17 @@ int check_attention(const tw::PagedAttention &p, size_t ws_bytes, const char *wh
         return fail(TW_ERR_BUFSIZE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
     if (!aligned(p.ws, 16))
         return fail(TW_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+    // what one block writes no other may read or write
+    const int64_t n = 4 * p.requests, q = 4 * ((p.requests - 1) * p.ldq + p.heads * D);
+    const Bytes in[] = {{p.block_table, 4 * ((p.requests - 1) * p.table_stride + p.max_pages), "the block table"},
+                        {p.lengths, n, "lengths"}, {p.first, n, "first"}, {p.q, q, "q"}};
+    const Bytes out[] = {{p.out, 4 * ((p.requests - 1) * p.ldo + p.heads * D), "out"}, {p.lse, n * p.heads, "lse"},
+                         {p.ws, (int64_t)need, "the workspace"}};
+    for (int i = 0; i < 3; ++i) {
+        if ((rc = apart(out[i], in, i == 0 ? 3 : 4, who)) || (rc = apart(out[i], out + i + 1, 2 - i, who)) ||
+            (rc = apart_from_cache(out[i], p.cache, who)))
+            return rc;
+    }
     return TW_OK;
 }
 

@@ -94,3 +94,21 @@ def test_append_overlap_is_that_of_the_bytes(api, seed):  # noqa: F811
         assert (rc == SHAPE) == want and rc in (SHAPE, 6, 9), (rc, put, rows, api.tw_last_error())
         seen[want] += 1
     assert min(seen) > 50
+
+
+ATTEND = dict(q=addr(3), ldq=1536, requests=4, heads=12, cache=None, block_table=addr(4), max_pages=8, table_stride=8,
+              lengths=addr(5), first=addr(8), scale=0.1, out=addr(6), ldo=1536, lse=addr(9), ws=addr(7), ws_bytes=1 << 27,
+              stream=None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(lse=addr(6) + 64), dict(lse=addr(3)), dict(lse=addr(5) + 12), dict(lse=addr(8) - 188), dict(lse=addr(7) + 32),
+    dict(lse=addr(1)), dict(lse=addr(11) + 4), dict(out=addr(2) + 512), dict(out=addr(4)), dict(out=addr(5) - 16),
+    dict(out=addr(7) + 4096), dict(out=addr(12)), dict(ws=addr(3) + 64), dict(ws=addr(9) + 16), dict(ws=addr(1) + 16),
+    dict(ws=addr(4)), dict(lengths=addr(6)), dict(first=addr(9) + 4), dict(block_table=addr(7) + 128)])
+def test_attention_refuses_outputs_in_its_operands(api, bad):  # noqa: F811
+    c = api.KVCacheStruct(k=addr(1), v=addr(2), k_scale=addr(11), v_scale=addr(12), num_pages=10, page_size=16, kv_heads=2,
+                          head_dim=128, page_stride=16 * 256, token_stride=256, head_stride=128, dtype=2)
+    args = dict(ATTEND, cache=ctypes.addressof(c))
+    assert api.tw_paged_attention(*dict(args, **bad).values()) == SHAPE, api.tw_last_error()
+    assert b"overlaps" in api.tw_last_error()
