@@ -174,8 +174,7 @@ int check_attention(const tw::PagedAttention &p, size_t ws_bytes, const char *wh
                     (long long)p.requests, (long long)p.max_pages);
     if (!std::isfinite(p.scale))
         return fail(TW_ERR_NONFINITE, "%s: scale is not finite", who);
-    if (overlap(p.q, 4 * ((p.requests - 1) * p.ldq + p.heads * D), p.out,
-                4 * ((p.requests - 1) * p.ldo + p.heads * D)))
+    if (rows_overlap(p.out, 4 * p.ldo, 4 * p.heads * D, p.q, 4 * p.ldq, 4 * p.heads * D, p.requests))
         return fail(TW_ERR_SHAPE, "%s: out overlaps q", who);
     const size_t need = (size_t)tw::paged_attention_ws_bytes(D);
     if (!p.ws || ws_bytes < need)

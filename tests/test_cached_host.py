@@ -112,3 +112,18 @@ def test_attention_refuses_outputs_in_its_operands(api, bad):  # noqa: F811
     args = dict(ATTEND, cache=ctypes.addressof(c))
     assert api.tw_paged_attention(*dict(args, **bad).values()) == SHAPE, api.tw_last_error()
     assert b"overlaps" in api.tw_last_error()
+
+
+@pytest.mark.parametrize("over,taken", [
+    (dict(ldq=3200, out=addr(3) + 4 * 1536, ldo=3200), True), (dict(ldq=3200, out=addr(3) + 4 * 1664, ldo=3200), True),
+    (dict(ldq=3200, out=addr(3) + 4 * 1532, ldo=3200), False), (dict(ldq=3200, out=addr(3) + 4 * 1668, ldo=3200), False),
+    (dict(ldq=3200, out=addr(3) + 4 * 1536, ldo=1536), False), (dict(out=addr(3)), False)])
+def test_attention_takes_rows_side_by_side(api, over, taken):  # noqa: F811
+    """Queries and outputs as columns of one buffer."""
+    import torch
+    if taken and torch.cuda.is_available():
+        pytest.skip("addresses of nothing: checked where nothing can be launched")
+    c = api.KVCacheStruct(k=addr(1), v=addr(2), num_pages=10, page_size=16, kv_heads=2, head_dim=128, page_stride=16 * 256,
+                          token_stride=256, head_stride=128)
+    rc = api.tw_paged_attention(*dict(ATTEND, cache=ctypes.addressof(c), **over).values())
+    assert rc in (6, 9) if taken else rc == SHAPE, api.tw_last_error()
