@@ -22,11 +22,21 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python -m ternary_weight_decoder_b200.build` "
         "(or __graft_entry__.build()); there is no CPU fallback")
 
+class _Missing:
+    """Stands for an extension module that does not load: whatever needs it raises."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs the extension module _bind, which is missing or does not load: build it "
+                          f"with `python -m ternary_weight_decoder_b200.build` ({self._why})")
+
+
 try:
     from . import _bind
-except ImportError as e:
-    raise ImportError("the extension module _bind is missing or does not load: build it with "
-                      f"`python -m ternary_weight_decoder_b200.build` ({e})") from e
+except ImportError as e:   # the operators of the paged cache and the norms are not there, all others are
+    _bind = _Missing(e)
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -513,9 +523,10 @@ tw_decoder_chain_cached = _sig("tw_decoder_chain_cached", _int,
 # ``_bind`` (csrc/tw_bind.cpp) checks their tensors, makes their outputs and
 # calls the entry points named above on the tensors' device and its current
 # stream.
-_bind.init(TernaryError, *(ctypes.cast(f, _p).value for f in (
-    tw_kv_assign, tw_rope_append, tw_paged_attention, tw_paged_attention_workspace_bytes,
-    tw_residual_norm, tw_last_error)))
+if not isinstance(_bind, _Missing):
+    _bind.init(TernaryError, *(ctypes.cast(f, _p).value for f in (
+        tw_kv_assign, tw_rope_append, tw_paged_attention, tw_paged_attention_workspace_bytes,
+        tw_residual_norm, tw_last_error)))
 
 
 def _on(stream, used, fn, *args):
