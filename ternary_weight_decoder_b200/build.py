@@ -5,12 +5,13 @@ header under ``csrc/`` or ``include/`` is newer), then linked with the static
 CUDA runtime into ``libternary_decoder.so`` next to this file.
 ``csrc/tw_bind.cpp``, the argument marshalling that works on torch tensors,
 becomes the extension module ``_bind.so`` beside it (the host compiler and
-torch's own headers and libraries).
+torch's own headers and libraries; rebuilt for another torch or Python too).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -22,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libternary_decoder.so")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_MADE_FOR = os.path.join(BUILD, "bind.made_for")   # the torch, Python and CUDA of that
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -40,11 +42,26 @@ def _newest(paths):
     return max((os.path.getmtime(p) for p in paths), default=0.0)
 
 
+def bind_made_for() -> str:
+    """What the extension module's binary interface depends on beside its source."""
+    return "\n".join(["torch " + importlib.metadata.version("torch"), str(sysconfig.get_config_var("SOABI")),
+                      _nvcc()])
+
+
+def bind_is_current() -> bool:
+    if not os.path.exists(BIND) or not os.path.exists(BIND_MADE_FOR):
+        return False
+    with open(BIND_MADE_FOR) as f:
+        if f.read() != bind_made_for():
+            return False
+    return os.path.getmtime(BIND) >= _newest([os.path.join(CSRC, "tw_bind.cpp")] +
+                                             glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
 def build_bind() -> None:
-    src = os.path.join(CSRC, "tw_bind.cpp")
-    if os.path.exists(BIND) and os.path.getmtime(BIND) >= _newest(
-            [src] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
+    if bind_is_current():
         return
+    src = os.path.join(CSRC, "tw_bind.cpp")
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -62,6 +79,8 @@ def build_bind() -> None:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("g++ failed: " + " ".join(cmd))
     os.replace(tmp, BIND)
+    with open(BIND_MADE_FOR, "w") as f:
+        f.write(bind_made_for())
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:

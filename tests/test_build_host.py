@@ -52,3 +52,17 @@ def test_library_is_built_without_the_extension(build, tmp_path, monkeypatch):
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         build.build()
     assert lib.stat().st_size > 0
+
+
+def test_extension_is_built_anew_for_another_torch(build, monkeypatch):
+    assert build.bind_is_current()
+    with monkeypatch.context() as m:
+        m.setattr(build.importlib.metadata, "version", lambda name: "0.0.1")
+        assert not build.bind_is_current()
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-0")
+        assert not build.bind_is_current()
+    with monkeypatch.context() as m:
+        m.setattr(build, "BIND_MADE_FOR", build.BIND_MADE_FOR + ".none")
+        assert not build.bind_is_current()
+    assert build.bind_is_current()
