@@ -664,7 +664,9 @@ TW_API int tw_residual_norm(const tw_residual_norm_args *args, tw_stream_t strea
  *   x = x + down(SiLU(gate(h1)) * up(h1))
  * and behind the last layer h = rms(x) * norm_out.  The tables are those of
  * tw_chain_layer, with q's y = q and k's y = k.  M requests; positions, slots
- * and lengths as tw_kv_assign writes them for one new token each.  hidden is
+ * and lengths as tw_kv_assign writes them for one new token each, row r for
+ * request r (its rows are packed: where some requests take no token, request
+ * r's are at row_start[r], and a request without one gets slot -1).  hidden is
  * at most 32768, as the norms' K.  Every table is checked before anything is
  * launched.
  */

@@ -719,8 +719,11 @@ class CachedDecoderChain(DecoderChain):
     the new token), ``positions`` [M] and ``slots`` [M] are int32 tensors that
     every run reads, row r for request r, as ``kv_assign`` fills them for one
     new token each.  Where some requests take none, its rows are packed:
-    request r's slot is then ``slots[row_start[r]]`` if it took a token and -1
-    if it did not (its row still runs, and changes no cache)."""
+    request r's slot and position are then ``slots[row_start[r]]`` and
+    ``positions[row_start[r]]`` if it took a token (``row_start[r + 1]`` is
+    past ``row_start[r]``), and -1 and ``lengths[r] - 1``, or any other, if it
+    did not (its row still runs, attends with what it has, and changes no
+    cache).  hidden is at most 32768."""
 
     def __init__(self, layers, M: int, hidden: int, kv_dim: int, head_dim: int, inter: int, device,
                  caches, norms, norm_out, inv_freq, block_table, lengths, positions, slots,
