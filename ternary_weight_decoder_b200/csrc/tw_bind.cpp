@@ -145,6 +145,14 @@ float real(PyObject *o, const char *name)
     return (float)v;
 }
 
+bool truth(PyObject *o)
+{
+    const int is = PyObject_IsTrue(o);
+    if (is < 0)
+        throw Refused{};   // (the object's own error)
+    return is;
+}
+
 // Outputs are made below the dispatcher, and parts of one buffer below the
 // tracking of views (the parts do not overlap and each is an output of its
 // own): kv_assign took 8.9 us with both, 7.2 without.
@@ -268,6 +276,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args)
         const at::Tensor &slots = dense(a[4], at::kInt, {n}, "slots", index);
         const double *freq = dense_or_null<double>(a[7], at::kDouble, {-1}, "inv_freq", index);
         const int64_t rotary = a[7] == Py_None ? 0 : 2 * THPVariable_Unpack(a[7]).size(0);
+        const bool interleaved = truth(a[8]);
         Rows to;
         if (a[9] != Py_None)
             to = rows(a[9], n, width, "q_out", index);
@@ -278,7 +287,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n_args)
             to = Rows{made.data_ptr<float>(), width};
         }
         raise_on(entry.rope_append(qr.p, qr.ld, kr.p, kr.ld, vr.p, vr.ld, n, heads, rotary, freq,
-                                   PyObject_IsTrue(a[8]), positions.data_ptr<int32_t>(), slots.data_ptr<int32_t>(),
+                                   interleaved, positions.data_ptr<int32_t>(), slots.data_ptr<int32_t>(),
                                    cache, to.p, to.ld, place.stream));
         return THPVariable_Wrap(given_or(a[9], made));
     });
@@ -302,7 +311,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args)
         if (a[7] != Py_None)
             to = rows(a[7], n, width, "out", index);
         float *lse = dense_or_null<float>(a[8], at::kFloat, {n, heads}, "lse", index);
-        const bool want_lse = PyObject_IsTrue(a[10]);
+        const bool want_lse = truth(a[10]);
         if (a[9] != Py_None)
             dense(a[9], at::kByte, {-1}, "ws", index);
         Place place(index);
@@ -336,7 +345,7 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n_args)
         const at::Tensor &x = THPVariable_Unpack(a[0]);
         matrix(x, "x");
         const int64_t M = x.size(0), K = x.size(1);
-        const bool quantize = PyObject_IsTrue(a[13]);
+        const bool quantize = truth(a[13]);
         tw_residual_norm_args g{};
         g.M = M, g.K = K;
         auto take = [&](PyObject *o, const char *name, auto &p, int64_t &ld) {
