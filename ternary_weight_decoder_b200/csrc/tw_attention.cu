@@ -1300,8 +1300,9 @@ cudaError_t launch_type(const PagedAttention &a, uint32_t *err, cudaStream_t str
 
 bool paged_attention_fits(int64_t requests, int64_t heads, int64_t kv_heads, int64_t max_pages, int64_t page_size)
 {
-    return requests * kv_heads * ceil_div(heads / kv_heads, kHeads) *
-               ceil_div(key_cap(max_pages, page_size), kMinTile) <= INT32_MAX;
+    // (each factor is below 2^31; the whole product need not fit 64 bits)
+    const int64_t units = requests * kv_heads * ceil_div(heads / kv_heads, kHeads);   // up to 2^24 * 2^16
+    return units <= INT32_MAX / ceil_div(key_cap(max_pages, page_size), kMinTile);
 }
 
 // Counters per head (one for each piece, one for each block), then maxima and sums, then sums of

@@ -127,3 +127,13 @@ def test_attention_takes_rows_side_by_side(api, over, taken):  # noqa: F811
                           token_stride=256, head_stride=128)
     rc = api.tw_paged_attention(*dict(ATTEND, cache=ctypes.addressof(c), **over).values())
     assert rc in (6, 9) if taken else rc == SHAPE, api.tw_last_error()
+
+
+def test_attention_counts_its_tiles_past_64_bits(api):  # noqa: F811
+    """2^24 requests of 2^16 heads with 2^24 tiles of 96 keys each: 2^64 tiles are too many, not none."""
+    c = api.KVCacheStruct(k=addr(1), v=addr(2), num_pages=10, page_size=12288, kv_heads=1 << 16, head_dim=8,
+                          page_stride=12288 << 19, token_stride=1 << 19, head_stride=8)
+    big = dict(requests=1 << 24, heads=1 << 16, ldq=1 << 19, ldo=1 << 19, lse=None, first=None, max_pages=1 << 17,
+               table_stride=1 << 17)
+    assert api.tw_paged_attention(*dict(ATTEND, cache=ctypes.addressof(c), **big).values()) == SHAPE
+    assert b"too many" in api.tw_last_error()
