@@ -608,9 +608,9 @@ TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads
  * queries to no less than 2^-23 of their head's largest and, on TW_KV_F16 and
  * TW_KV_I8, weights (times their value's scale) to no less than 2^-37 of the
  * largest (or 2^-117 of the sum of weights, where that is more).
- * TW_KV_I8: the scales of visible keys and values are 0 or in
- * [2^-60, 2^60]; where keys whose value has a scale of 0 outweigh the others'
- * weights times scales by 2^80, lse is off by up to 2^-16.
+ * TW_KV_I8: the scales of visible keys and values are in [0, 2^60]; where keys
+ * whose value has a scale below 2^-80, or 0, outweigh the others' weights times
+ * scales by 2^80, lse is off by up to 2^-16.
  * heads: a multiple of kv_heads.
  */
 TW_API int tw_paged_attention(const float *q, int64_t ldq, int64_t requests, int64_t heads,

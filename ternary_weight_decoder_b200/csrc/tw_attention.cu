@@ -45,12 +45,12 @@ constexpr int kHeads = 8;                    // query heads of a unit
 constexpr int kFan = 16;                     // pieces that half a warp joins, of one head
 constexpr int kMinTile = 96;                 // keys of the smallest variant's tile
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-// log2 of a value's scale of 0, as far as the running maximum goes: such a key
-// adds to the sum of weights alone.  Below the smallest scale (2^-60), so that
-// the others' weights keep their bits unless theirs are below 2^-80 of its
-// own; not lower, as a weight is then 2^(80 + 12 + 3) at most, and the fp32
-// sum of 2^31 of them finite.
-constexpr float kNoScale = -80.f;
+// The least log2 of a value's scale, as far as the running maximum goes: a key
+// with a smaller one, or 0, adds to the sum of weights and hardly to the values.
+// So low that the others' weights times scales keep their bits unless they are
+// below 2^-80 of such a key's weight; not lower, as that is then 2^(80 + 12 + 3)
+// at most, and the fp32 sum of 2^31 of them finite.
+constexpr float kLeastScale = -80.f;
 
 // A call, as the kernel reads it.
 struct Args {
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(Shape<DT, DP>::kThreads, Shape<DT, DP>::kBlock
                         const float ks = of[16 * h + 8 * k];
                         s[h][2 * k] *= ks, s[h][2 * k + 1] *= ks;
                         vs[h][k] = of[S::kKeys + 16 * h + 8 * k];
-                        lv[h][k] = vs[h][k] > 0.f ? __log2f(vs[h][k]) : kNoScale;
+                        lv[h][k] = fmaxf(__log2f(vs[h][k]), kLeastScale);
                     }
             }
             if (mask != S::kAll) {

@@ -102,3 +102,31 @@ def test_every_scale_zero(dev, api):
     cache.v[:, :, 1] = 3
     cache.v_scale[:, :, 1] = 0.01
     check(api, dev, cache, q, table, lengths, 12, dominant=True)
+
+
+@pytest.mark.parametrize("heads,hk,d,page", SHAPES)
+@pytest.mark.parametrize("low,high", [(-62, -60), (-85, -75), (-126, -100), (-126, -122), (-126, 0)])
+def test_scales_below_the_products_range(dev, api, heads, hk, d, page, low, high):
+    """Scales of all keys far below 1: sums stay finite, outputs within 2^-117 of the sum of weights."""
+    lengths = [64, 1, 300, 6000]
+    cache, q, table = make(api, dev, "i8", lengths, heads, hk, d, page, 70 + d, poison=False)
+    rng = np.random.default_rng(d)
+    cache.v_scale.copy_(G.to_dev((2.0 ** rng.uniform(low, high, tuple(cache.v_scale.shape))).astype(np.float32), dev))
+    check(api, dev, cache, q, table, lengths, heads, dominant=True)
+
+
+def test_tiny_values_appended_and_read(dev, api):
+    """Scales as the append makes them from values of 1e-20 and 1e-35, beside a row of zeros."""
+    import torch
+    page, hk, d, n = 16, 2, 64, 40
+    cache = api.KVCache.empty(4, page, hk, d, torch.int8, dev)
+    rng = np.random.default_rng(5)
+    k, v = (rng.standard_normal((n, hk * d)).astype(np.float32) for _ in range(2))
+    v[:20] *= 1e-20
+    v[20:] *= 1e-35
+    v[7] = 0
+    q = rng.standard_normal((n, 4 * d)).astype(np.float32)
+    api.rope_append(G.to_dev(q, dev), G.to_dev(k, dev), G.to_dev(v, dev), i32(range(n), dev), i32(range(n), dev), cache)
+    for length in (n, 8, 1):
+        check(api, dev, cache, q[-1:], np.arange(4)[None], [length], 4, dominant=True)
+    check(api, dev, cache, q[-1:], np.array([[2, 1, 0, 3]]), [13], 4, dominant=True)   # the smallest alone
