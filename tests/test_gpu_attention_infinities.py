@@ -48,17 +48,17 @@ def formula(q, k, v, scale):
     return out, lse[0], tol[0], tl[0]
 
 
-def check(api, dev, cache, q, table, lengths, heads):
+def check(api, dev, cache, q, table, lengths, heads, first=None):
     d, group = cache.head_dim, heads // cache.kv_heads
     ws = api.paged_attention_workspace(len(lengths), heads, cache)
-    args = (G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev))
+    args = (G.to_dev(q, dev), cache, i32(table, dev), i32(lengths, dev), None if first is None else i32(first, dev))
     for _ in range(2):
         out, lse = api.paged_attention(*args, ws=ws, return_lse=True)
         api.check()
         out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
         seen = set()
         for r, n in enumerate(lengths):
-            k, v = rows_of(cache, table, r, 0, n)
+            k, v = rows_of(cache, table, r, 0 if first is None else min(max(first[r], 0), n), n)
             for h in range(heads):
                 want, wl, tol, tl = formula(q[r, h * d:(h + 1) * d].astype(np.float64), k[:, h // group],
                                             v[:, h // group], d ** -0.5)
@@ -119,6 +119,24 @@ def test_infinite_queries(dev, api, dtype, heads, hk, d, page):
     for j in range(LENGTHS[5]):
         put(cache.k, table, 5, j, 0, 11, 1 + j % 3)
     check(api, dev, cache, q, table, LENGTHS, heads)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("seed", range(6))
+def test_infinities_anywhere(dev, api, dtype, seed):
+    """Many requests with windows, a few runs' ends in each, infinities at random places seen or not."""
+    rng = np.random.default_rng(100 + seed)
+    heads, hk, d, page = SHAPES[seed]
+    count = int(rng.integers(20, 90))
+    lengths = [int(n) for n in rng.integers(0, int(rng.choice([200, 700, 2500])), count)]
+    first = [int(rng.integers(-5, n + 3)) if rng.random() < 0.5 else 0 for n in lengths]
+    cache, q, table = make(api, dev, dtype, lengths, heads, hk, d, page, seed, first=first)
+    for _ in range(count):
+        r = int(rng.integers(0, count))
+        if lengths[r]:
+            j, h, c = int(rng.integers(0, lengths[r])), int(rng.integers(0, hk)), int(rng.integers(0, d))
+            put(cache.k if rng.random() < 0.3 else cache.v, table, r, j, h, c, float(rng.choice([np.inf, -np.inf])))
+    check(api, dev, cache, q, table, lengths, heads, first)
 
 
 def test_fp16_keys_past_its_range(dev, api):
