@@ -29,10 +29,10 @@
 // units of eight, which read their keys again (from L2, mostly).
 //
 // Measured on B200 (12 heads over 2 KV heads of 128): past the first 262144
-// keys of one request, another 262144 take 36.9 us of bf16 (7.3 TB/s) and
-// 21.2 us of codes (6.7 TB/s), the memory's rate; what is left is the start
-// (scanning lengths, looking up pages, the first keys: about 5 us) and the
-// joins (2 to 6 us).
+// keys of one request, another 262144 take 37 .. 41 us of bf16 or fp16 (6.6 ..
+// 7.2 TB/s, of which L2 gives some) and 21.9 us of codes with their scales (6.3
+// TB/s), the memory's rate; what is left is the start (scanning lengths, looking
+// up pages, the first keys: about 5 us) and the joins (2 to 6 us).
 #include <cfloat>
 
 #include "tw_kv.cuh"
@@ -89,7 +89,8 @@ struct Shape {
     // columns), so that its fixed instructions count for less.  14 heads over 2
     // of 64 columns: 119 requests of 121 .. 231 keys 9.9 us (16 a step: 12.8),
     // 14 of 11500 .. 73268 49.1 us (50.7); but 212 of 24 .. 32 over 8 heads
-    // 20.4 us (17.4), as fewer steps are on their way.
+    // 20.4 us (17.4), as fewer steps are on their way (the host, which chooses,
+    // does not know the lengths).
     static constexpr int kHalves = kCodes || DP <= 64 ? 2 : 1;
     static constexpr int kKeys = 16 * kHalves;
     static constexpr uint32_t kAll = kHalves == 2 ? 0xffffffffu : 0xffffu;

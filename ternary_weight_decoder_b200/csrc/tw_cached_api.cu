@@ -195,7 +195,7 @@ int check_attention(const tw::PagedAttention &p, size_t ws_bytes, const char *wh
     return TW_OK;
 }
 
-// heads query heads over kv_heads, at most 2^20 query rows in all.
+// Up to 2^24 rows of up to 2^16 query heads, an equal number for each KV head.
 int check_heads(int64_t rows, int64_t heads, int64_t kv_heads, const char *who)
 {
     if (rows < 1 || rows > (1 << 24))

@@ -16,7 +16,12 @@ namespace {
 // ------------------------------------------------------------- assignment
 constexpr int kAsThreads = 1024;
 constexpr int kAsCtas = 16;         // one cluster (of the largest size), or
-constexpr int64_t kAsSmall = 2800;  // a single block up to as many requests and rows
+// a single block up to as many requests and rows: more requests would not fit
+// the shared memory that needs no asking (32 requests and rows 5.2 us, the
+// cluster 5.8; 1400 of each 8.0, 8.8; 32 and 2700 rows 6.0, 6.7.  The cluster is
+// ahead from some 5000 rows on: 32 and 4000 rows 7.2 us, a block 6.5; 6000 rows
+// 7.0, 8.1).
+constexpr int64_t kAsSmall = 2800;
 
 __device__ __forceinline__ uint32_t pages_of(int32_t len, uint32_t page)   // len >= 0
 {
@@ -55,7 +60,9 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane)
 // One cluster of blocks.  Every block scans all requests for itself
 // (at most kAssignMaxRequests lengths, read from L2), so that the only thing
 // the blocks wait for is that the pages handed back are in the free list
-// before any page is taken from it.  Pages and rows then go out thread by
+// before any page is taken from it.  Bound by that: two passes over the requests
+// with divisions by the page size and 64-bit sums, the same in every block, then
+// dependent loads and bisections (1024 requests and 65536 rows: 10.8 us for 0.8 MB).  Pages and rows then go out thread by
 // thread: each finds its request by bisection of the prefix sums in shared
 // memory, and a row its page in the block table or, where this step takes it,
 // straight in the free list.
@@ -237,8 +244,8 @@ __global__ void __launch_bounds__(kAsThreads) k_kv_assign(const KvAssign a, uint
 // -------------------------------------------------- rotation and the cache
 constexpr int kRaThreads = 256;
 // Warps that a call is split into before a warp takes more heads: 32 on each
-// of 148 SMs (8192 rows of 12 + 2 + 2 heads, 126 MB: one row a warp 24.9 us,
-// half a row 27.5 us, a quarter 31.6 us).
+// of 148 SMs (8192 rows of 12 + 2 + 2 heads, 126 MB, in turn with two others:
+// one row a warp 24.9 us, half a row 27.5 us, a quarter 31.6 us).
 constexpr int64_t kRaWarps = 4736;
 
 // Sine and cosine of pos * freq.  The angle is formed in 64 bits and brought
@@ -246,8 +253,8 @@ constexpr int64_t kRaWarps = 4736;
 // in two 64-bit parts, each product fused with its sum; adding 1.5 * 2^52
 // rounds to a whole number and leaves it in the low bits).  What is left, r,
 // is rounded to 32 bits, by at most 2^-25, so that far positions are as exact
-// as near ones; its Taylor series end below 2^-33 (r^11 / 11! and r^12 / 12!
-// at pi/4).  k mod 4 swaps and signs the two.
+// as near ones; its Taylor series leave out less than 2^-29 (sine, r^11 / 11! at
+// pi/4) and 2^-33 (cosine, r^12 / 12!).  k mod 4 swaps and signs the two.
 __device__ __forceinline__ void angle_sincos(int32_t pos, double freq, float *sin_out, float *cos_out)
 {
     const double kQuarterHi = 1.5707963267948966, kQuarterLo = 6.123233995736766e-17;
@@ -284,8 +291,9 @@ __device__ __forceinline__ void store4(void *base, int64_t at, float4 v)
 // A warp takes `per` consecutive heads (of q, then k, then v) of one row: a
 // lane holds QUADS groups of four consecutive columns and makes the cosines
 // and sines that they need once for all of the heads, so nothing is shared
-// and kBatch heads are in flight at a time.  Bound by memory; what has to be
-// kept down is the instructions for a head.
+// and kBatch heads are in flight at a time.  Large calls wait for their loads with
+// two fifths of the warps resident (64 registers): 8192 rows of 12 + 2 + 2 heads,
+// 126 MB of which L2 holds nothing, take 25.8 us (4.9 TB/s; into codes 28.2).
 constexpr int kBatch = 4;
 template <int DT, int QUADS, bool PAIRS>   // PAIRS: (2i, 2i + 1) are turned, else (i, i + rotary / 2)
 __global__ void __launch_bounds__(kRaThreads, QUADS == 1 ? 4 : 2) k_rope_append(const RopeAppend a, int per,

@@ -9,14 +9,19 @@
 //
 // A row is read once: y (or x alone) into registers, x and a gate per token
 // meanwhile into registers, shared memory or L2; sums are in 32 bits, the
-// variance from the centred values.  Bound by memory, 16 bytes per element (x,
-// y in; h, n out): 4096 rows of 1536 with both norms and a gate take 19.2 us
-// (5.2 TB/s), of 8960 in 1000 rows 30.0 us (4.8 TB/s); odd widths, column by
-// column, about 0.6 of that.  Measured and left out: persistent blocks with the
-// next rows on their way into shared memory (24.9 and 47.1 us: with one row at
-// a time in a block the reductions' latency shows), a warp a row (35.1 us at
-// 1536), odd widths in groups of four between memory's boundaries with their
-// ends apart (2492 rows of 2407: 33 us, single columns 26 us).
+// variance from the centred values.  What it has to move is 16 bytes per element
+// (x, y in; h, n out).  4096 rows of 1536 with both norms and a gate take 21.9 us
+// where L2 holds nothing of them (4.6 TB/s; 19.8 us into buffers that it holds),
+// of 8960 in 1000 rows 37.5 us (3.8 TB/s), odd widths, column by column, 30 .. 45 us
+// for as many bytes.  That is not the memory's rate (6.5 TB/s): a row's reductions
+// and barriers leave too few bytes on their way, and 1000 rows in three blocks an
+// SM are two and a quarter turns of the GPU.  Where nothing else is said, the times
+// of one choice against another below are of passes whose outputs L2 holds.
+// Measured and left out: persistent blocks with the next rows on their way into
+// shared memory (24.9 and 47.1 us: with one row at a time in a block the
+// reductions' latency shows), a warp a row (35.1 us at 1536), odd widths in groups
+// of four between memory's boundaries with their ends apart (2492 rows of 2407:
+// 33 us, single columns 26 us).
 #include "tw_device.cuh"
 #include "tw_internal.h"
 #include "tw_kv.cuh"
@@ -24,6 +29,7 @@
 namespace tw {
 namespace {
 
+constexpr int64_t kSms = 148;   // of a B200
 
 // Sums (or maxima) over the threads of a row, in a fixed order: the lanes by
 // butterfly, then the warps' values by butterfly in every warp.  The warps'
@@ -362,9 +368,9 @@ bool by16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 cudaError_t launch_quads(const ResidualNorm &a, cudaStream_t stream)
 {
     const int64_t groups = a.K / 4;
-    if (groups <= 512 && a.M <= 2 * 148)
+    if (groups <= 512 && a.M <= 2 * kSms)
         return launch<4, 1>(a, stream);
-    if (a.M < 148) {
+    if (a.M < kSms) {
         if (groups <= 1024)
             return launch<4, 1, 1024>(a, stream);
         if (groups <= 2048)
@@ -392,9 +398,9 @@ cudaError_t launch_quads(const ResidualNorm &a, cudaStream_t stream)
 // Odd widths and strides.
 cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
 {
-    if (a.K <= 1024 && a.M <= 2 * 148)
+    if (a.K <= 1024 && a.M <= 2 * kSms)
         return launch<1, 1, 1024>(a, stream);
-    if (a.M < 148) {
+    if (a.M < kSms) {
         if (a.K <= 2048)
             return launch<1, 2, 1024>(a, stream);
         if (a.K <= 4096)
@@ -405,7 +411,11 @@ cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
     // eight columns a thread (3903 rows of 1537: 26 us, four 39 us), more in
     // rows that 512 threads cannot hold so
     if (a.K <= 256)   // a warp a row where there are rows enough (4096 of 171: 5.9 us, 128 threads 7.5; 300: 4.1, 3.0)
-        return a.M > 12 * 148 ? launch_all<1, 8, 32, 32>(a, stream) : launch_all<1, 2, 128>(a, stream);
+        return a.M > 12 * kSms ? launch_all<1, 8, 32, 32>(a, stream) : launch_all<1, 2, 128>(a, stream);
+    // As few threads as hold the row so: of 512 most would have no column (6.3
+    // million values in rows of 385, 601, 901, 1301, 1601, 2201 and 2559 columns,
+    // nothing in L2: 30, 30, 30, 29, 30, 31 and 31 us, with 512 threads 122, 83, 59,
+    // 45, 40, 35 and 33).
     if (a.K <= 512)
         return launch_all<1, 4, 128>(a, stream);
     if (a.K <= 1024)
@@ -418,6 +428,11 @@ cudaError_t launch_singles(const ResidualNorm &a, cudaStream_t stream)
         return launch_all<1, 8, 320>(a, stream);
     if (a.K <= 4096)
         return launch_all<1, 8, 512>(a, stream);
+    // Rows waiting in shared memory, three blocks an SM (nothing in L2): with a gate
+    // per token, layer norms and codes 1280 rows of 4687 take 42.0 us, with sixteen
+    // columns a thread and two blocks 53.9, 300 rows 15.7 and 23.3; with a gate per
+    // column and RMS norms 38.1 and 38.5, 300 rows 15.3 and 18.9 (976 of 6143: 45.4
+    // and 40.8).
     if (a.K <= 6144)
         return launch_shared<1, 12, 3, 512, 512>(a, stream);
     if (a.K <= 8192)
