@@ -562,14 +562,13 @@ TW_API int tw_kv_assign(const int32_t *lengths, const int32_t *delta, int64_t re
  * in fp64), the pair i being columns (i, i + rotary/2), or (2i, 2i + 1) when
  * interleaved:  (a, b) -> (a cos - b sin, b cos + a sin) in fp32.  q_out
  * (row stride ldqo; may be q with the same stride, else shares no byte with
- * q's, k's or v's rows, which may be columns of one buffer with it, nor with the
- * cache, positions, slots or inv_freq) receives every row's queries.
- * Keys and values of a row with slots[t] < 0 are not written; a
- * slot at or past the end of the pools records TW_ERR_CORRUPT and is not
- * written either.  Slots of different rows must differ.  TW_KV_I8: amax =
- * max |x| over the head, code = clamp(rint(x * (127.0f / amax)), -127, 127),
- * scale = amax / 127.0f (amax == 0: code 0); non-finite values give
- * unspecified codes.
+ * q's, k's or v's rows, which may be columns of one buffer with it, nor with
+ * the cache, positions, slots or inv_freq) receives every row's queries.  Keys
+ * and values of a row with slots[t] < 0 are not written; a slot at or past the
+ * end of the pools records TW_ERR_CORRUPT and is not written either.  Slots of
+ * different rows must differ.  TW_KV_I8: amax = max |x| over the head, code =
+ * clamp(rint(x * (127.0f / amax)), -127, 127), scale = amax / 127.0f (amax ==
+ * 0: code 0); non-finite values give unspecified codes.
  * rotary: a multiple of 8, 0 <= rotary <= head_dim (0: inv_freq unused).
  */
 TW_API int tw_rope_append(const float *q, int64_t ldq, const float *k, int64_t ldk, const float *v,
@@ -592,25 +591,26 @@ TW_API size_t tw_paged_attention_workspace_bytes(int64_t requests, int64_t heads
  * max(0, first[r]) <= j < lengths[r] (first NULL: from 0):
  *   s_j = scale * (q_i . k_j);  m = max s_j
  *   out_i = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m);  lse_i = m + log sum_j e^(s_j - m)
- * A request that sees no key gets out = 0 and lse = -inf.  out has row stride
- * ldo; lse [requests x heads] may be NULL; out, lse and the workspace share no
- * byte with one another, the cache or an input.  Nothing outside the visible keys
- * is used, whatever its pages hold.  Visible infinities and NaN (an fp16 cache
- * holds infinities for what is past its range) give what the formula gives in
- * fp32: an infinite value in its column, NaN beside one of the other sign or
- * where its weight is below fp32's range; no weight for a score of -inf (a
- * head with no other score: 0 and -inf); NaN for a score of +inf.  Pieces of
- * requests that hold some are computed twice, the second time slowly.
- * A length past max_pages * page_size and
- * a page outside the pools record TW_ERR_CORRUPT: the keys concerned are left
- * out.  Sums and softmax statistics are fp32; the products' operands are
- * carried with at least 21 significant bits (cache elements exactly), but
- * queries to no less than 2^-23 of their head's largest and, on TW_KV_F16 and
- * TW_KV_I8, weights (times their value's scale) to no less than 2^-37 of the
- * largest (or 2^-117 of the sum of weights, where that is more).
- * TW_KV_I8: the scales of visible keys and values are in [0, 2^60]; where keys
- * whose value has a scale below 2^-80, or 0, outweigh the others' weights times
- * scales by 2^80, lse is off by up to 2^-16.
+ * A request that sees no key gets out = 0 and lse = -inf. out has row
+ * stride ldo; lse [requests x heads] may be NULL; out, lse and the
+ * workspace share no byte with one another, the cache or an input. Nothing
+ * outside the visible keys is used, whatever its pages hold.
+ * Visible infinities and NaN (an fp16 cache holds infinities for what is
+ * past its range) give what the formula gives in fp32: an infinite value in
+ * its column, NaN beside one of the other sign or where its weight is below
+ * fp32's range; no weight for a score of -inf (a head with no other score:
+ * 0 and -inf); NaN for a score of +inf. Pieces of requests that hold some
+ * are computed twice, the second time slowly.
+ * A length past max_pages * page_size and a page outside the pools record
+ * TW_ERR_CORRUPT: the keys concerned are left out.
+ * Sums and softmax statistics are fp32; the products' operands are carried
+ * with at least 21 significant bits (cache elements exactly), but queries
+ * to no less than 2^-23 of their head's largest and, on TW_KV_F16 and
+ * TW_KV_I8, weights (times their value's scale) to no less than 2^-37 of
+ * the largest (or 2^-117 of the sum of weights, where that is more).
+ * TW_KV_I8: the scales of visible keys and values are in [0, 2^60]; where
+ * keys whose value has a scale below 2^-80, or 0, outweigh the others'
+ * weights times scales by 2^80, lse is off by up to 2^-16.
  * heads: a multiple of kv_heads.
  */
 TW_API int tw_paged_attention(const float *q, int64_t ldq, int64_t requests, int64_t heads,

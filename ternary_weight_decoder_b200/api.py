@@ -643,7 +643,8 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     """Rotate q [rows, heads * head_dim] and k [rows, kv_heads * head_dim] by
     positions [rows] * inv_freq [rotary / 2] (fp64; None: no rotation), write
     k and v into the cache at slots [rows] (negative: not written) and return
-    the rotated queries (``q_out``; may be q).  Rows may be strided."""
+    the rotated queries (``q_out``; may be q, else shares no byte with an
+    operand or the cache).  Rows may be strided."""
     if stream is not None:
         return _on(stream, (q, k, v, positions, slots, inv_freq, q_out) + cache.tensors, rope_append,
                    q, k, v, positions, slots, cache, inv_freq, interleaved, q_out)
@@ -667,7 +668,8 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     over keys max(0, first[r]) .. lengths[r] - 1 of its pages in block_table
     [requests, max_pages]; scale is 1 / sqrt(head_dim) by default.  Returns out,
     or (out, lse) with the log-sum-exps [requests, heads].  ``ws`` comes from
-    ``paged_attention_workspace`` (None: one is made for the call)."""
+    ``paged_attention_workspace`` (None: one is made for the call).  ``out``,
+    ``lse`` and ``ws`` share no byte with an operand or the cache."""
     if stream is not None:
         return _on(stream, (q, block_table, lengths, first, out, lse, ws) + cache.tensors, paged_attention,
                    q, cache, block_table, lengths, first, scale, out, lse, ws, return_lse)
